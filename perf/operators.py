@@ -263,15 +263,17 @@ def _own(s):
     case, op = s["case"], s["case"]["op"]
     if op == "norm":
         moe.moe_block_norm(s["y"], s["x_out"], residual=s["residual"], alpha=case["alpha"], gate=s["gate"],
-                           w_post=s["w_post"], w_next=s["w_next"], normed=s["normed"], eps=EPS)
+                           gate_mode=case["gate"], w_post=s["w_post"], w_next=s["w_next"], normed=s["normed"],
+                           eps=EPS)
         return s["x_out"], s["normed"]
     if op == "norm_grad":
         if "ws" not in s:                       # a program keeps its workspace
             s["ws"] = moe.alloc_ws(moe.block_norm_backward_workspace_size(case["T"], case["D"]))
         moe.moe_block_norm_backward(s["dx_out"], s["dnormed"], s["x_out"], s["y"], s["dy"], s["ws"],
-                                    dresidual=s["dresidual"], alpha=case["alpha"], gate=s["gate"], dgate=s["dgate"],
-                                    w_post=s["w_post"], dw_post=s["dw_post"], rstd_post=s["rstd_post"],
-                                    w_next=s["w_next"], dw_next=s["dw_next"], rstd_next=s["rstd_next"])
+                                    dresidual=s["dresidual"], alpha=case["alpha"], gate=s["gate"],
+                                    gate_mode=case["gate"], dgate=s["dgate"], w_post=s["w_post"],
+                                    dw_post=s["dw_post"], rstd_post=s["rstd_post"], w_next=s["w_next"],
+                                    dw_next=s["dw_next"], rstd_next=s["rstd_next"])
         return s["dy"], s["dresidual"], s["dgate"], s["dw_post"], s["dw_next"]
     if op == "permute":
         moe.moe_permute(s["ids"], case["E"], s["offsets"], s["pair_row"], s["row_pair"], x=s["x"], rows=s["rows"],
