@@ -1,4 +1,4 @@
-"""Thin ctypes binding of ``libmoe.so`` (include/moe.h).
+"""Thin ctypes binding of ``libmoe.so`` (include/moe.h, moe_cache.h, moe_ops.h).
 
 Argument marshalling only: every step of the expert pass runs in the CUDA
 library.  Tensors are torch CUDA tensors; their device pointers and the current
@@ -22,13 +22,16 @@ LIB_PATH = os.path.join(_HERE, "libmoe.so")
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUDA, MOE_ERR_TIMEOUT, MOE_ERR_RANGE = \
     0, -1, -2, -3, -4, -5, -6
 MOE_Q2_32, MOE_Q3_32, MOE_Q3_S256 = 0, 1, 2
+MOE_BF16, MOE_F16, MOE_F32 = 0, 1, 2
 
 EXPORTS = ["moe_slot_code_bytes", "moe_slot_scale_bytes", "moe_route_workspace_size", "moe_workspace_size",
            "moe_expert_out_size", "moe_route_topk", "moe_expert_forward", "moe_combine", "moe_dequantize",
            "moe_status_string", "moe_route_topk_static", "moe_expert_hist", "moe_cache_plan", "moe_slot_fill",
            "moe_workspace_status", "moe_debug_wait_flag", "moe_debug_operand_workspace_size",
            "moe_debug_prefill_operand", "moe_layer_workspace_size", "moe_layer_forward",
-           "moe_workspace_size_fp8", "moe_expert_forward_fp8"]
+           "moe_workspace_size_fp8", "moe_expert_forward_fp8", "moe_permute", "moe_permute_backward",
+           "moe_unpermute", "moe_unpermute_backward", "moe_route_backward", "moe_route_backward_workspace_size",
+           "moe_block_norm", "moe_block_norm_backward", "moe_block_norm_backward_workspace_size"]
 
 
 class MoeError(RuntimeError):
@@ -97,6 +100,25 @@ def lib():
         L.moe_layer_forward.restype = i
         L.moe_layer_forward.argtypes = [ctypes.POINTER(moe_pool), P, i, P, i, P, P, i, P, P, P, sz, P, P, P, P, P, sz,
                                         P]
+        f = ctypes.c_float
+        L.moe_permute.restype = i
+        L.moe_permute.argtypes = [P, i, i, i, P, i, P, i, i, P, P, P, P, P]
+        L.moe_permute_backward.restype = i
+        L.moe_permute_backward.argtypes = [P, i, P, i, i, i, i, P, P]
+        L.moe_unpermute.restype = i
+        L.moe_unpermute.argtypes = [P, i, P, P, i, i, i, i, P, i, P]
+        L.moe_unpermute_backward.restype = i
+        L.moe_unpermute_backward.argtypes = [P, i, P, i, P, P, i, i, i, i, P, P, P]
+        L.moe_route_backward_workspace_size.restype = sz
+        L.moe_route_backward_workspace_size.argtypes = [i, i, i, i]
+        L.moe_route_backward.restype = i
+        L.moe_route_backward.argtypes = [P, P, P, P, P, P, P, i, i, i, i, P, P, P, P, P, P, sz, P]
+        L.moe_block_norm.restype = i
+        L.moe_block_norm.argtypes = [P, P, P, i, f, P, P, f, i, i, i, P, P, P, P, P]
+        L.moe_block_norm_backward_workspace_size.restype = sz
+        L.moe_block_norm_backward_workspace_size.argtypes = [i, i]
+        L.moe_block_norm_backward.restype = i
+        L.moe_block_norm_backward.argtypes = [P, P, P, P, P, i, f, P, P, P, P, i, i, i, P, P, P, P, P, P, sz, P]
         L.moe_status_string.restype = ctypes.c_char_p
         L.moe_status_string.argtypes = [i]
         _lib = L
@@ -268,6 +290,154 @@ def moe_slot_fill(pool: moe_pool, slot, host_codes, host_scales, stream=None):
             raise ValueError("host_codes / host_scales must be contiguous host tensors")
     _check("moe_slot_fill", lib().moe_slot_fill(ctypes.byref(pool), int(slot), ctypes.c_void_p(host_codes.data_ptr()),
                                                 ctypes.c_void_p(host_scales.data_ptr()), _stream(stream)))
+
+
+# The operators of moe_ops.h.  The tensors of a call lie on one device, which
+# need not be the current one; the call goes to `stream` or to that device's
+# current stream.
+_DTYPES = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32}
+_GATE_MODES = {None: 0, "none": 0, "channel": 1, "token": 2}
+_I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
+
+
+def _dtype(name, t):
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be bfloat16, float16 or float32, not {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+def _arg(name, t, dtype, shape, device):
+    """The device address of a contiguous tensor of this type and shape (0 for None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, not "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', strided'}")
+    return t.data_ptr()
+
+
+def _call(fn, device, stream, *args):
+    if device.type != "cuda":
+        raise ValueError(f"{fn} takes CUDA tensors, not tensors on {device}")
+    if stream is not None and stream.device != device:
+        raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on {device}")
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _call(fn, device, stream, *args)
+    handle = (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    st = getattr(lib(), fn)(*args, handle)
+    if st != MOE_OK:
+        raise MoeError(fn, st)
+
+
+def moe_permute(ids, E, offsets, pair_row, row_pair, x=None, rows=None, slot_table=None, n_slots=0, stream=None):
+    """Tokens sorted by expert: rows[i] = x[row_pair[i] // k], grouped by expert (all pairs, or with slot_table the
+    missed ones).  Without x and rows only the plan (offsets, pair_row, row_pair) is made."""
+    T, k = ids.shape
+    dev = ids.device
+    dt, D = (MOE_BF16, 1) if x is None else (_dtype("x", x), x.shape[-1])
+    _call("moe_permute", dev, stream, _arg("ids", ids, _I32, (T, k), dev), T, k, E,
+          _arg("slot_table", slot_table, _I32, (E,), dev), n_slots,
+          None if x is None else _arg("x", x, x.dtype, (T, D), dev), D, dt,
+          None if x is None and rows is None else _arg("rows", rows, rows.dtype if x is None else x.dtype, (T * k, D),
+                                                       dev),
+          _arg("offsets", offsets, _I32, (E + 1,), dev), _arg("pair_row", pair_row, _I32, (T, k), dev),
+          _arg("row_pair", row_pair, _I32, (T * k,), dev))
+
+
+def moe_permute_backward(drows, pair_row, dx, stream=None):
+    """dx[t] = the sum of drows over token t's rows."""
+    T, k = pair_row.shape
+    n, D = drows.shape
+    dev = drows.device
+    _call("moe_permute_backward", dev, stream, _arg("drows", drows, drows.dtype, (n, D), dev), n,
+          _arg("pair_row", pair_row, _I32, (T, k), dev), T, k, D, _dtype("drows", drows),
+          _arg("dx", dx, drows.dtype, (T, D), dev))
+
+
+def moe_unpermute(rows, pair_row, out, weights=None, stream=None):
+    """out[t] = the sum of weights[t, r] * rows[pair_row[t, r]]; out of rows' type or float32 (a miss_partial)."""
+    T, k = pair_row.shape
+    n, D = rows.shape
+    dev = rows.device
+    _call("moe_unpermute", dev, stream, _arg("rows", rows, rows.dtype, (n, D), dev), n,
+          _arg("pair_row", pair_row, _I32, (T, k), dev), _arg("weights", weights, _F32, (T, k), dev), T, k, D,
+          _dtype("rows", rows), _arg("out", out, out.dtype, (T, D), dev), _dtype("out", out))
+
+
+def moe_unpermute_backward(dout, pair_row, drows=None, rows=None, weights=None, dweights=None, stream=None):
+    """drows[pair_row[t, r]] = weights[t, r] * dout[t] and dweights[t, r] = <dout[t], rows[pair_row[t, r]]>."""
+    T, k = pair_row.shape
+    like = drows if drows is not None else rows
+    if like is None:
+        raise ValueError("moe_unpermute_backward writes drows, dweights (from rows), or both")
+    n, D = like.shape
+    dev = dout.device
+    _call("moe_unpermute_backward", dev, stream, _arg("dout", dout, dout.dtype, (T, D), dev), _dtype("dout", dout),
+          _arg("rows", rows, like.dtype, (n, D), dev), n, _arg("pair_row", pair_row, _I32, (T, k), dev),
+          _arg("weights", weights, _F32, (T, k), dev), T, k, D, _dtype("rows", like),
+          _arg("drows", drows, like.dtype, (n, D), dev), _arg("dweights", dweights, _F32, (T, k), dev))
+
+
+def route_backward_workspace_size(T, D, E, k) -> int:
+    return int(lib().moe_route_backward_workspace_size(T, D, E, k))
+
+
+def moe_route_backward(dgates, gates, ids, x, Wr, offsets, row_pair, dlogits, ws, dx=None, dx_add=None, dWr=None,
+                       dbias=None, stream=None):
+    """Gradient of moe_route_topk's gates; offsets and row_pair are moe_permute's of the same ids (no slot_table)."""
+    T, k = ids.shape
+    E, D = Wr.shape
+    dev = ids.device
+    _call("moe_route_backward", dev, stream, _arg("dgates", dgates, _F32, (T, k), dev),
+          _arg("gates", gates, _F32, (T, k), dev), _arg("ids", ids, _I32, (T, k), dev),
+          _arg("x", x, _BF16, (T, D), dev), _arg("Wr", Wr, _BF16, (E, D), dev),
+          _arg("offsets", offsets, _I32, (E + 1,), dev), _arg("row_pair", row_pair, _I32, (T * k,), dev), T, D, E, k,
+          _arg("dx_add", dx_add, _BF16, (T, D), dev), _arg("dlogits", dlogits, _F32, (T, k), dev),
+          _arg("dx", dx, _BF16, (T, D), dev), _arg("dWr", dWr, _F32, (E, D), dev),
+          _arg("dbias", dbias, _F32, (E,), dev), _arg("ws", ws, torch.uint8, ws.shape, dev), ws.numel())
+
+
+def _gate(gate, gate_mode, T, D):
+    if gate_mode not in _GATE_MODES:
+        raise ValueError(f"gate_mode must be 'none', 'channel' or 'token', not {gate_mode!r}")
+    mode = _GATE_MODES[gate_mode]
+    return mode, (T,) if mode == 2 else (D,)
+
+
+def moe_block_norm(y, x_out=None, residual=None, alpha=1.0, gate=None, gate_mode=None, w_post=None, w_next=None,
+                   normed=None, rstd_post=None, rstd_next=None, eps=1e-6, stream=None):
+    """x_out = alpha * residual + gate * norm(y) * w_post (y itself without w_post); normed = norm(x_out) * w_next.
+    gate_mode: 'channel' (gate [D]) or 'token' (gate [T])."""
+    T, D = y.shape
+    dev, dt = y.device, y.dtype
+    mode, gs = _gate(gate, gate_mode, T, D)
+    _call("moe_block_norm", dev, stream, _arg("y", y, dt, (T, D), dev), _arg("residual", residual, dt, (T, D), dev),
+          _arg("gate", gate, _F32, gs, dev), mode, alpha, _arg("w_post", w_post, _F32, (D,), dev),
+          _arg("w_next", w_next, _F32, (D,), dev), eps, T, D, _dtype("y", y), _arg("x_out", x_out, dt, (T, D), dev),
+          _arg("normed", normed, dt, (T, D), dev), _arg("rstd_post", rstd_post, _F32, (T,), dev),
+          _arg("rstd_next", rstd_next, _F32, (T,), dev))
+
+
+def block_norm_backward_workspace_size(T, D) -> int:
+    return int(lib().moe_block_norm_backward_workspace_size(T, D))
+
+
+def moe_block_norm_backward(dx_out, dnormed, x_out, y, dy, ws, dresidual=None, alpha=1.0, gate=None, gate_mode=None,
+                            dgate=None, w_post=None, dw_post=None, rstd_post=None, w_next=None, dw_next=None,
+                            rstd_next=None, stream=None):
+    """Gradients of moe_block_norm; the arguments left None there stay None here, as do gradients not wanted."""
+    T, D = dy.shape
+    dev, dt = dy.device, dy.dtype
+    mode, gs = _gate(gate, gate_mode, T, D)
+    _call("moe_block_norm_backward", dev, stream, _arg("dx_out", dx_out, dt, (T, D), dev),
+          _arg("dnormed", dnormed, dt, (T, D), dev), _arg("x_out", x_out, dt, (T, D), dev),
+          _arg("y", y, dt, (T, D), dev), _arg("gate", gate, _F32, gs, dev), mode, alpha,
+          _arg("w_post", w_post, _F32, (D,), dev), _arg("rstd_post", rstd_post, _F32, (T,), dev),
+          _arg("w_next", w_next, _F32, (D,), dev), _arg("rstd_next", rstd_next, _F32, (T,), dev), T, D,
+          _dtype("dy", dy), _arg("dy", dy, dt, (T, D), dev), _arg("dresidual", dresidual, dt, (T, D), dev),
+          _arg("dgate", dgate, _F32, gs, dev), _arg("dw_post", dw_post, _F32, (D,), dev),
+          _arg("dw_next", dw_next, _F32, (D,), dev), _arg("ws", ws, torch.uint8, ws.shape, dev), ws.numel())
 
 
 class Layer:
