@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(NormArgs a) {
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            v[i][j] = to_f32(from_f32<T>(v[i][j]));         // x_out as it is stored
+            v[i][j] = as_stored<T>(v[i][j]);         // x_out as it is stored
             ss = __fmaf_rn(v[i][j], v[i][j], ss);
         }
         if (a.x_out) store_f32<T, V>(static_cast<T*>(a.x_out) + at + c, v[i]);

@@ -8,6 +8,7 @@
 //   permute backward   the same sum with w = 1, of the rows' gradients
 //   unpermute backward drows[row(p)] = w[p] dout[t],  dw[p] = <dout[t], rows[row(p)]>
 // Every one of them moves each row once and each token once: HBM bounds them.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -18,189 +19,328 @@
 namespace moe {
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanBlocks = 8;             // one cluster
+constexpr int kPlanHeld = 8;               // rounds of 32 pairs that a warp keeps in registers between its walks
+constexpr int kSmallPairs = 4096;          // up to here every block makes its part of the plan itself
+constexpr int kSmallThreads = 256;
+constexpr int kNoExpert = 0x7fffffff;
 
-// The expert of pair p, or -1 if the pair is not taken.
+// The expert of pair p, or kNoExpert if the pair is not taken.
 MOE_DEVINL int taken_expert(const int32_t* ids, int p, int E, const int32_t* slot_table, int n_slots) {
     const int e = __ldg(ids + p);
-    if (e < 0 || e >= E) return -1;
+    if (e < 0 || e >= E) return kNoExpert;
     if (slot_table) {
         const int s = __ldg(slot_table + e);
-        if (s >= 0 && s < n_slots) return -1;
+        if (s >= 0 && s < n_slots) return kNoExpert;
     }
     return e;
 }
 
-// The plan: a stable counting sort of the P pairs by expert in one block.  Warp
-// w owns the pairs of segment w, 32 at a time in order; lanes with the same
-// expert find one another (match), the first of them adds their number to the
-// warp's counter of that expert.  An exclusive scan over (expert, warp) turns
-// the counters into first rows, and the second walk over the pairs hands them out.
-__global__ void __launch_bounds__(kPlanThreads) permute_plan_kernel(const int32_t* __restrict__ ids, int P, int E,
-                                                                    const int32_t* __restrict__ slot_table,
-                                                                    int n_slots, int32_t* __restrict__ offsets,
-                                                                    int32_t* __restrict__ pair_row,
-                                                                    int32_t* __restrict__ row_pair) {
-    extern __shared__ int32_t count[];          // [warp][E]
-    __shared__ int wsum[32];
-    pdl_wait();
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    for (int i = threadIdx.x; i < kPlanWarps * E; i += kPlanThreads) count[i] = 0;
-    __syncthreads();
-    const int seg = ((P + kPlanWarps - 1) / kPlanWarps + 31) / 32 * 32;
-    const int p0 = w * seg, p1 = min(P, p0 + seg);
-    int32_t* mine = count + w * E;
-    for (int p = p0; p < p1; p += 32) {
-        const int e = p + lane < p1 ? taken_expert(ids, p + lane, E, slot_table, n_slots) : -1;
-        const uint32_t peers = __match_any_sync(0xffffffffu, e);
-        if (e >= 0 && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
-        __syncwarp();
-    }
-    __syncthreads();
-    // thread e: the expert's total, and its warps' counters as offsets inside the expert
-    int total = 0;
-    if (threadIdx.x < E) {
-        for (int i = 0; i < kPlanWarps; ++i) {
-            const int c = count[i * E + threadIdx.x];
-            count[i * E + threadIdx.x] = total;
-            total += c;
-        }
-    }
-    int incl = total;
+// Inclusive prefix sum over the block's threads (a multiple of 32, at most 1024).
+MOE_DEVINL int block_scan(int v, int* wsum) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
+        const int y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
     }
-    if (lane == 31) wsum[w] = incl;
+    if (lane == 31) wsum[w] = v;
     __syncthreads();
-    if (w == 0) {
-        int t = wsum[lane];
+    int s = lane < w && lane < nw ? wsum[lane] : 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, t, o);
-            if (lane >= o) t += y;
+    for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return v + s;
+}
+
+// The plan: a stable counting sort of the P pairs by expert, in one cluster.
+// Warp w of block b owns the pairs of segment (b, w), 32 at a time in order;
+// lanes with the same expert find one another (match), the first of them adds
+// their number to the warp's counter of that expert.  An exclusive scan over
+// (expert, block, warp) turns the counters into first rows, and a second walk
+// over the pairs hands them out.  A chain of memory latencies bounds it, so the
+// ids of up to 8 rounds are loaded together and kept for the second walk.
+__global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThreads)
+    permute_plan_kernel(const int32_t* __restrict__ ids, int P, int E, const int32_t* __restrict__ slot_table,
+                        int n_slots, int32_t* __restrict__ offsets, int32_t* __restrict__ pair_row,
+                        int32_t* __restrict__ row_pair) {
+    extern __shared__ int32_t count[];          // [warp][E]
+    __shared__ int block_total[kOpsMaxE];       // of each expert, read by the cluster's other blocks
+    __shared__ int wsum[32];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, b = (int)cluster.block_rank();
+    for (int i = threadIdx.x; i < kPlanWarps * E; i += kPlanThreads) count[i] = 0;
+    pdl_wait();
+    __syncthreads();
+    const int rounds = (P + kPlanBlocks * kPlanThreads - 1) / (kPlanBlocks * kPlanThreads);
+    const int p0 = (b * kPlanWarps + w) * rounds * 32 + lane;
+    int32_t* mine = count + w * E;
+    int held[kPlanHeld];
+    for (int i0 = 0; i0 < rounds; i0 += kPlanHeld) {
+#pragma unroll
+        for (int i = 0; i < kPlanHeld; ++i) {
+            const int p = p0 + (i0 + i) * 32;
+            held[i] = i0 + i < rounds && p < P ? taken_expert(ids, p, E, slot_table, n_slots) : kNoExpert;
         }
-        wsum[lane] = t;
+#pragma unroll
+        for (int i = 0; i < kPlanHeld; ++i) {
+            if (i0 + i >= rounds) break;
+            const uint32_t peers = __match_any_sync(0xffffffffu, held[i]);
+            if (held[i] != kNoExpert && lane == __ffs(peers) - 1) mine[held[i]] += __popc(peers);
+            __syncwarp();
+        }
     }
     __syncthreads();
+    // thread e: the expert's total in this block, and its warps' counters as offsets inside it
+    int in_block = 0;
     if (threadIdx.x < E) {
-        const int base = incl - total + (w ? wsum[w - 1] : 0);
-        offsets[threadIdx.x] = base;
-        if (threadIdx.x == E - 1) offsets[E] = base + total;
-        for (int i = 0; i < kPlanWarps; ++i) count[i * E + threadIdx.x] += base;
+#pragma unroll 8
+        for (int i = 0; i < kPlanWarps; ++i) {
+            const int c = count[i * E + threadIdx.x];
+            count[i * E + threadIdx.x] = in_block;
+            in_block += c;
+        }
+        block_total[threadIdx.x] = in_block;
     }
-    __syncthreads();
-    for (int p = p0; p < p1; p += 32) {
-        const int e = p + lane < p1 ? taken_expert(ids, p + lane, E, slot_table, n_slots) : -1;
-        const uint32_t peers = __match_any_sync(0xffffffffu, e);
-        int row = -1;
-        if (e >= 0) row = mine[e] + __popc(peers & ((1u << lane) - 1u));
-        __syncwarp();
-        if (e >= 0 && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
-        __syncwarp();
-        if (p + lane < p1) {
-            pair_row[p + lane] = row;
-            if (row >= 0) row_pair[row] = p + lane;
+    cluster.sync();
+    int total = 0, before = 0;
+    if (threadIdx.x < E) {
+#pragma unroll
+        for (int i = 0; i < kPlanBlocks; ++i) {
+            const int c = cluster.map_shared_rank(block_total, i)[threadIdx.x];
+            total += c;
+            if (i < b) before += c;
+        }
+    }
+    const int base = block_scan(total, wsum) - total;
+    if (threadIdx.x < E) {
+        if (b == 0) {
+            offsets[threadIdx.x] = base;
+            if (threadIdx.x == E - 1) offsets[E] = base + total;
+        }
+#pragma unroll 8
+        for (int i = 0; i < kPlanWarps; ++i) count[i * E + threadIdx.x] += base + before;
+    }
+    cluster.sync();                             // no block leaves while another reads its totals
+    for (int i0 = 0; i0 < rounds; i0 += kPlanHeld) {
+        if (rounds > kPlanHeld) {
+#pragma unroll
+            for (int i = 0; i < kPlanHeld; ++i) {
+                const int p = p0 + (i0 + i) * 32;
+                held[i] = i0 + i < rounds && p < P ? taken_expert(ids, p, E, slot_table, n_slots) : kNoExpert;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kPlanHeld; ++i) {
+            const int p = p0 + (i0 + i) * 32;
+            if (i0 + i >= rounds) break;
+            const uint32_t peers = __match_any_sync(0xffffffffu, held[i]);
+            int row = -1;
+            if (held[i] != kNoExpert) row = mine[held[i]] + __popc(peers & ((1u << lane) - 1u));
+            __syncwarp();
+            if (held[i] != kNoExpert && lane == __ffs(peers) - 1) mine[held[i]] += __popc(peers);
+            __syncwarp();
+            if (p < P) {
+                pair_row[p] = row;
+                if (row >= 0) row_pair[row] = p;
+            }
         }
     }
 }
 
-// rows[pair_row[t][r]] = x[t]: one block per token, the token read once.
+// x[t] into the rows row[0..k): the token is read once.
 template <typename T, int V>
-__global__ void __launch_bounds__(256) permute_rows_kernel(const T* __restrict__ x,
-                                                           const int32_t* __restrict__ pair_row, int k, int D,
-                                                           T* __restrict__ rows) {
-    pdl_wait();
-    const int t = blockIdx.x;
+MOE_DEVINL void scatter_token(const T* x, int t, const int32_t* row, int k, int D, T* rows) {
     for (int c = threadIdx.x * V; c < D; c += blockDim.x * V) {
         const Pack<T, V> a = load_pack<T, V>(x + (size_t)t * D + c);
-        for (int r = 0; r < k; ++r) {
-            const int row = __ldg(pair_row + t * k + r);
-            if (row >= 0) store_pack<T, V>(rows + (size_t)row * D + c, a);
-        }
+        for (int r = 0; r < k; ++r)
+            if (row[r] >= 0) store_pack<T, V>(rows + (size_t)row[r] * D + c, a);
     }
 }
 
-// out[t] = sum_r w[t,r] rows[row(t,r)], r ascending in fp32 (w NULL: 1).
-template <typename T, typename TO, int V>
-__global__ void __launch_bounds__(256) unpermute_kernel(const T* __restrict__ rows, int n_rows,
+// A small batch in one launch: block t places the pairs of token t itself, by
+// counting the pairs that come before each of them (a warp per pair, the pairs'
+// experts in shared memory), then copies its token; block T writes the offsets.
+template <typename T, int V>
+__global__ void __launch_bounds__(kSmallThreads) permute_small_kernel(
+    const int32_t* __restrict__ ids, int P, int E, const int32_t* __restrict__ slot_table, int n_slots,
+    const T* __restrict__ x, int k, int D, T* __restrict__ rows, int32_t* __restrict__ offsets,
+    int32_t* __restrict__ pair_row, int32_t* __restrict__ row_pair) {
+    __shared__ __align__(16) int key[kSmallPairs];
+    __shared__ int hist[kOpsMaxE];
+    __shared__ int32_t row[kMaxTopK];
+    __shared__ int wsum[32];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, t = blockIdx.x;
+    const bool last = t == (int)gridDim.x - 1;
+    if (last)
+        for (int e = threadIdx.x; e < E; e += kSmallThreads) hist[e] = 0;
+    pdl_wait();
+    const int P4 = (P + 3) / 4;
+    for (int p = threadIdx.x; p < P4 * 4; p += kSmallThreads)
+        key[p] = p < P ? taken_expert(ids, p, E, slot_table, n_slots) : kNoExpert;
+    __syncthreads();
+    if (last) {
+        for (int p = threadIdx.x; p < P; p += kSmallThreads)
+            if (key[p] != kNoExpert) atomicAdd(hist + key[p], 1);
+        __syncthreads();
+        constexpr int N = kOpsMaxE / kSmallThreads;
+        int c[N], sum = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int e = threadIdx.x * N + i;
+            c[i] = e < E ? hist[e] : 0;
+            sum += c[i];
+        }
+        int at = block_scan(sum, wsum) - sum;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int e = threadIdx.x * N + i;
+            if (e < E) offsets[e] = at;
+            at += c[i];
+            if (e == E - 1) offsets[E] = at;
+        }
+        return;
+    }
+    for (int r = w; r < k; r += kSmallThreads / 32) {
+        const int p = t * k + r, e = key[p];
+        int n = 0;
+        for (int q = lane; q < P4; q += 32) {
+            const int4 v = reinterpret_cast<const int4*>(key)[q];
+            const int vs[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) n += vs[j] < e || (vs[j] == e && q * 4 + j < p);
+        }
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (e == kNoExpert) n = -1;
+        if (lane == 0) {
+            row[r] = n;
+            pair_row[p] = n;
+            if (n >= 0) row_pair[n] = p;
+        }
+    }
+    if (!x) return;
+    __syncthreads();
+    scatter_token<T, V>(x, t, row, k, D, rows);
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(512) permute_rows_kernel(const T* __restrict__ x,
+                                                           const int32_t* __restrict__ pair_row, int k, int D,
+                                                           T* __restrict__ rows) {
+    __shared__ int32_t row[kMaxTopK];
+    pdl_wait();
+    const int t = blockIdx.x;
+    if (threadIdx.x < k) row[threadIdx.x] = __ldg(pair_row + t * k + threadIdx.x);
+    __syncthreads();
+    scatter_token<T, V>(x, t, row, k, D, rows);
+}
+
+// out[t] = sum_r w[t,r] rows[row(t,r)], r ascending in fp32 (w NULL: 1).  A
+// thread owns U packs of the token, blockDim apart, and loads them from up to R
+// rows before it adds the first.
+template <typename T, typename TO, int V, int U, int R>
+__global__ void __launch_bounds__(128) unpermute_kernel(const T* __restrict__ rows, int n_rows,
                                                         const int32_t* __restrict__ pair_row,
                                                         const float* __restrict__ weights, int k, int D,
                                                         TO* __restrict__ out) {
     pdl_wait();
     const int t = blockIdx.x;
-    for (int c = threadIdx.x * V; c < D; c += blockDim.x * V) {
-        float acc[V];
+    const int c0 = (blockIdx.y * U * 128 + threadIdx.x) * V;
+    float acc[U][V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = 0.f;
-        for (int r = 0; r < k; ++r) {
-            const int row = __ldg(pair_row + t * k + r);
-            if (row < 0 || row >= n_rows) continue;
-            const float w = weights ? __ldg(weights + t * k + r) : 1.f;
-            float y[V];
-            load_f32<T, V>(rows + (size_t)row * D + c, y);
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = __fmaf_rn(w, y[i], acc[i]);
+        for (int i = 0; i < V; ++i) acc[u][i] = 0.f;
+    int row[R];
+    float w[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        row[r] = r < k ? __ldg(pair_row + t * k + r) : -1;
+        w[r] = r < k && weights ? __ldg(weights + t * k + r) : 1.f;
+    }
+    Pack<T, V> y[U][R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if (row[r] >= n_rows) row[r] = -1;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = c0 + u * 128 * V;
+            if (row[r] >= 0 && c < D) y[u][r] = load_pack<T, V>(rows + (size_t)row[r] * D + c);
         }
-        store_f32<TO, V>(out + (size_t)t * D + c, acc);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int c = c0 + u * 128 * V;
+        if (c >= D) continue;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (row[r] < 0) continue;
+            float v[V];
+            unpack<T, V>(y[u][r], v);
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[u][i] = __fmaf_rn(w[r], v[i], acc[u][i]);
+        }
+        store_f32<TO, V>(out + (size_t)t * D + c, acc[u]);
     }
 }
 
-// drows[row(t,r)] = w[t,r] dout[t] and dw[t,r] = <dout[t], rows[row(t,r)]>.
-template <typename T, typename TO, int V>
+// drows[row(p)] = w[p] dout[t] and dw[p] = <dout[t], rows[row(p)]>: a warp per
+// pair, U packs in flight per lane.  The k warps of a token read dout[t] after
+// one another, so all but the first find it in the caches.
+template <typename T, typename TO, int V, int U>
 __global__ void __launch_bounds__(256) unpermute_backward_kernel(const TO* __restrict__ dout,
                                                                  const T* __restrict__ rows, int n_rows,
                                                                  const int32_t* __restrict__ pair_row,
-                                                                 const float* __restrict__ weights, int k, int D,
+                                                                 const float* __restrict__ weights, int P, int k, int D,
                                                                  T* __restrict__ drows, float* __restrict__ dweights) {
-    __shared__ float part[kMaxTopK][8];
     pdl_wait();
-    const int t = blockIdx.x, lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
-    float dot[kMaxTopK];
+    const int p = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (p >= P) return;
+    const int row = __ldg(pair_row + p);
+    const bool held = row >= 0 && row < n_rows;
+    float dot = 0.f;
+    if (held) {
+        const float w = weights ? __ldg(weights + p) : 1.f;
+        const TO* d = dout + (size_t)(p / k) * D;
+        const size_t at = (size_t)row * D;
+        for (int c0 = lane * V; c0 < D; c0 += U * 32 * V) {
+            Pack<T, V> y[U];
+            float g[U][V];
 #pragma unroll
-    for (int r = 0; r < kMaxTopK; ++r) dot[r] = 0.f;
-    for (int c = threadIdx.x * V; c < D; c += blockDim.x * V) {
-        float d[V];
-        load_f32<TO, V>(dout + (size_t)t * D + c, d);
+            for (int u = 0; u < U; ++u)
+                if (c0 + u * 32 * V < D && dweights) y[u] = load_pack<T, V>(rows + at + c0 + u * 32 * V);
 #pragma unroll
-        for (int r = 0; r < kMaxTopK; ++r) {
-            if (r >= k) continue;
-            const int row = __ldg(pair_row + t * k + r);
-            if (row < 0 || row >= n_rows) continue;
-            if (dweights) {
-                float y[V];
-                load_f32<T, V>(rows + (size_t)row * D + c, y);
+            for (int u = 0; u < U; ++u)
+                if (c0 + u * 32 * V < D) load_f32<TO, V>(d + c0 + u * 32 * V, g[u]);
 #pragma unroll
-                for (int i = 0; i < V; ++i) dot[r] = __fmaf_rn(d[i], y[i], dot[r]);
-            }
-            if (drows) {
-                const float w = weights ? __ldg(weights + t * k + r) : 1.f;
-                float g[V];
+            for (int u = 0; u < U; ++u) {
+                if (c0 + u * 32 * V >= D) continue;
+                if (dweights) {
+                    float v[V];
+                    unpack<T, V>(y[u], v);
 #pragma unroll
-                for (int i = 0; i < V; ++i) g[i] = w * d[i];
-                store_f32<T, V>(drows + (size_t)row * D + c, g);
+                    for (int i = 0; i < V; ++i) dot = __fmaf_rn(g[u][i], v[i], dot);
+                }
+                if (drows) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) g[u][i] *= w;
+                    store_f32<T, V>(drows + at + c0 + u * 32 * V, g[u]);
+                }
             }
         }
+        dot = warp_sum(dot);
     }
-    if (!dweights) return;
-#pragma unroll
-    for (int r = 0; r < kMaxTopK; ++r) {
-        if (r >= k) continue;
-        const float s = warp_sum(dot[r]);
-        if (lane == 0) part[r][wp] = s;
-    }
-    __syncthreads();
-    if (threadIdx.x < k) {
-        float s = 0.f;
-        for (int i = 0; i < (int)(blockDim.x >> 5); ++i) s += part[threadIdx.x][i];
-        dweights[(size_t)t * k + threadIdx.x] = s;
-    }
+    if (dweights && lane == 0) dweights[p] = dot;
 }
 
-// Threads for a row of n packs: one pack per thread, whole warps, at most 256.
-inline int row_threads(int n) { return n >= 256 ? 256 : (n + 31) / 32 * 32; }
+// Threads for a row of n packs: whole warps, at most 512, the row's passes equally full.
+inline int row_threads(int n) {
+    const int passes = (n + 511) / 512;
+    return ((n + passes - 1) / passes + 31) / 32 * 32;
+}
 
 // Rows whose bytes are a multiple of 16, in 16-byte aligned buffers.
 template <typename... P>
@@ -208,18 +348,25 @@ inline bool wide_rows(int D, size_t elem, P... p) {
     return (D * elem) % 16 == 0 && (ops_aligned(p, 16) && ...);
 }
 
-template <typename T, typename TO, int V>
+template <typename T, typename TO, int V, int U>
 cudaError_t run_unpermute(const void* rows, int n_rows, const int32_t* pair_row, const float* weights, int T_, int k,
                           int D, void* out, cudaStream_t s) {
-    return launch_pdl(unpermute_kernel<T, TO, V>, dim3(T_), dim3(row_threads((D + V - 1) / V)), 0, s,
-                      static_cast<const T*>(rows), n_rows, pair_row, weights, k, D, static_cast<TO*>(out));
+    const dim3 grid(T_, (D + U * 128 * V - 1) / (U * 128 * V));
+    auto go = [&](auto kernel) {
+        return launch_pdl(kernel, grid, dim3(128), 0, s, static_cast<const T*>(rows), n_rows, pair_row, weights, k, D,
+                          static_cast<TO*>(out));
+    };
+    if (k <= 4) return go(unpermute_kernel<T, TO, V, U, 4>);
+    if (k <= 8) return go(unpermute_kernel<T, TO, V, U, 8>);
+    if (k <= 12) return go(unpermute_kernel<T, TO, V, U, 12>);
+    return go(unpermute_kernel<T, TO, V, U, 16>);
 }
-template <typename T, typename TO, int V>
+template <typename T, typename TO, int V, int U>
 cudaError_t run_unpermute_backward(const void* dout, const void* rows, int n_rows, const int32_t* pair_row,
-                                   const float* weights, int T_, int k, int D, void* drows, float* dweights,
+                                   const float* weights, int P, int k, int D, void* drows, float* dweights,
                                    cudaStream_t s) {
-    return launch_pdl(unpermute_backward_kernel<T, TO, V>, dim3(T_), dim3(row_threads((D + V - 1) / V)), 0, s,
-                      static_cast<const TO*>(dout), static_cast<const T*>(rows), n_rows, pair_row, weights, k, D,
+    return launch_pdl(unpermute_backward_kernel<T, TO, V, U>, dim3((P + 7) / 8), dim3(256), 0, s,
+                      static_cast<const TO*>(dout), static_cast<const T*>(rows), n_rows, pair_row, weights, P, k, D,
                       static_cast<T*>(drows), dweights);
 }
 
@@ -230,11 +377,38 @@ moe_status launch_unpermute(const void* rows, int n_rows, const int32_t* pair_ro
         using T = decltype(e);
         constexpr int V = 16 / sizeof(T);
         if (out_dtype == MOE_F32)
-            return ops_status(wide ? run_unpermute<T, float, V>(rows, n_rows, pair_row, weights, T_, k, D, out, s)
-                                   : run_unpermute<T, float, 1>(rows, n_rows, pair_row, weights, T_, k, D, out, s));
-        return ops_status(wide ? run_unpermute<T, T, V>(rows, n_rows, pair_row, weights, T_, k, D, out, s)
-                               : run_unpermute<T, T, 1>(rows, n_rows, pair_row, weights, T_, k, D, out, s));
+            return ops_status(wide ? run_unpermute<T, float, V, 1>(rows, n_rows, pair_row, weights, T_, k, D, out, s)
+                                   : run_unpermute<T, float, 1, 4>(rows, n_rows, pair_row, weights, T_, k, D, out, s));
+        return ops_status(wide ? run_unpermute<T, T, V, 1>(rows, n_rows, pair_row, weights, T_, k, D, out, s)
+                               : run_unpermute<T, T, 1, 4>(rows, n_rows, pair_row, weights, T_, k, D, out, s));
     });
+}
+
+template <typename T>
+moe_status launch_permute(const int32_t* ids, int T_, int k, int E, const int32_t* slot_table, int n_slots,
+                          const T* x, int D, T* rows, int32_t* offsets, int32_t* pair_row, int32_t* row_pair,
+                          cudaStream_t s) {
+    constexpr int V = 16 / sizeof(T);
+    const int P = T_ * k;
+    const bool wide = wide_rows(D, sizeof(T), x, rows);
+    if (P <= kSmallPairs) {
+        auto kernel = wide ? permute_small_kernel<T, V> : permute_small_kernel<T, 1>;
+        return ops_status(launch_pdl(kernel, dim3(T_ + 1), dim3(kSmallThreads), 0, s, ids, P, E, slot_table, n_slots, x,
+                                     k, D, rows, offsets, pair_row, row_pair));
+    }
+    static std::atomic<uint64_t> set{0};
+    if (!once_per_device(set, [] {
+            return cudaFuncSetAttribute(permute_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        kPlanWarps * kOpsMaxE * 4) == cudaSuccess;
+        }))
+        return MOE_ERR_CUDA;
+    const cudaError_t e = launch_pdl(permute_plan_kernel, dim3(kPlanBlocks), dim3(kPlanThreads),
+                                     (size_t)kPlanWarps * E * 4, s, ids, P, E, slot_table, n_slots, offsets, pair_row,
+                                     row_pair);
+    if (e != cudaSuccess || !x) return ops_status(e);
+    auto kernel = wide ? permute_rows_kernel<T, V> : permute_rows_kernel<T, 1>;
+    return ops_status(launch_pdl(kernel, dim3(T_), dim3(row_threads(wide ? D / V : D)), 0, s, x,
+                                 (const int32_t*)pair_row, k, D, rows));
 }
 
 bool out_dtype_ok(int dtype, int out_dtype) { return out_dtype == dtype || out_dtype == MOE_F32; }
@@ -259,25 +433,10 @@ extern "C" moe_status moe_permute(const int32_t* ids, int T, int k, int E, const
     if (!ops_aligned(ids, 4) || !ops_aligned(pair_row, 4) || !ops_aligned(row_pair, 4) || !ops_aligned(slot_table, 4) ||
         !ops_aligned(x, es) || !ops_aligned(rows, es) || (x && x == rows))
         return MOE_ERR_INVALID_ARG;
-    static std::atomic<uint64_t> set{0};
-    if (!once_per_device(set, [] {
-            return cudaFuncSetAttribute(permute_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        kPlanWarps * kOpsMaxE * 4) == cudaSuccess;
-        }))
-        return MOE_ERR_CUDA;
-    cudaError_t e = launch_pdl(permute_plan_kernel, dim3(1), dim3(kPlanThreads), (size_t)kPlanWarps * E * 4, s, ids,
-                               T * k, E, slot_table, n_slots, offsets, pair_row, row_pair);
-    if (e != cudaSuccess || !x) return ops_status(e);
-    const bool wide = wide_rows(D, es, x, rows);
     return with_dtype(dtype, [&](auto el) {
         using Tp = decltype(el);
-        constexpr int V = 16 / sizeof(Tp);
-        const Tp* xt = static_cast<const Tp*>(x);
-        Tp* rt = static_cast<Tp*>(rows);
-        return ops_status(wide ? launch_pdl(permute_rows_kernel<Tp, V>, dim3(T), dim3(row_threads(D / V)), 0, s, xt,
-                                            (const int32_t*)pair_row, k, D, rt)
-                               : launch_pdl(permute_rows_kernel<Tp, 1>, dim3(T), dim3(row_threads(D)), 0, s, xt,
-                                            (const int32_t*)pair_row, k, D, rt));
+        return launch_permute<Tp>(ids, T, k, E, slot_table, n_slots, static_cast<const Tp*>(x), D,
+                                  static_cast<Tp*>(rows), offsets, pair_row, row_pair, s);
     });
 }
 
@@ -318,12 +477,15 @@ extern "C" moe_status moe_unpermute_backward(const void* dout, int out_dtype, co
     return with_dtype(dtype, [&](auto e) {
         using Tp = decltype(e);
         constexpr int V = 16 / sizeof(Tp);
+        const int P = T * k;
         if (out_dtype == MOE_F32)
-            return ops_status(
-                wide ? run_unpermute_backward<Tp, float, V>(dout, rows, n_rows, pair_row, weights, T, k, D, drows, dweights, s)
-                     : run_unpermute_backward<Tp, float, 1>(dout, rows, n_rows, pair_row, weights, T, k, D, drows, dweights, s));
-        return ops_status(
-            wide ? run_unpermute_backward<Tp, Tp, V>(dout, rows, n_rows, pair_row, weights, T, k, D, drows, dweights, s)
-                 : run_unpermute_backward<Tp, Tp, 1>(dout, rows, n_rows, pair_row, weights, T, k, D, drows, dweights, s));
+            return ops_status(wide ? run_unpermute_backward<Tp, float, V, 4>(dout, rows, n_rows, pair_row, weights, P, k,
+                                                                             D, drows, dweights, s)
+                                   : run_unpermute_backward<Tp, float, 1, 16>(dout, rows, n_rows, pair_row, weights, P,
+                                                                              k, D, drows, dweights, s));
+        return ops_status(wide ? run_unpermute_backward<Tp, Tp, V, 4>(dout, rows, n_rows, pair_row, weights, P, k, D,
+                                                                      drows, dweights, s)
+                               : run_unpermute_backward<Tp, Tp, 1, 16>(dout, rows, n_rows, pair_row, weights, P, k, D,
+                                                                       drows, dweights, s));
     });
 }

@@ -18,20 +18,19 @@ constexpr int kOpsMaxD = 8192;
 constexpr int kOpsMaxE = 1024;
 constexpr int kOpsMaxT = 65536;
 
-MOE_DEVINL float to_f32(float v) { return v; }
-MOE_DEVINL float to_f32(__half v) { return __half2float(v); }
-MOE_DEVINL float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-// Round to nearest even, the one rounding between an fp32 result and its store.
+// Round to nearest even: the one rounding between an fp32 result and its store.
 template <typename T> MOE_DEVINL T from_f32(float v);
 template <> MOE_DEVINL float from_f32<float>(float v) { return v; }
 template <> MOE_DEVINL __half from_f32<__half>(float v) { return __float2half_rn(v); }
 template <> MOE_DEVINL __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// V elements moved by one access (16 bytes, or one element: V = 1).
-template <typename T, int V>
-struct alignas(sizeof(T) * V) Pack {
-    T v[V];
-};
+// V elements moved by one access: 16 bytes, or one element (V = 1).  Packs of
+// 16-bit elements stay packed in 32-bit words until they are used.
+template <int BYTES> struct RawOf { using type = uint32_t; };
+template <> struct RawOf<2> { using type = uint16_t; };
+template <> struct RawOf<8> { using type = uint2; };
+template <> struct RawOf<16> { using type = uint4; };
+template <typename T, int V> using Pack = typename RawOf<V * (int)sizeof(T)>::type;
 
 template <typename T, int V>
 MOE_DEVINL Pack<T, V> load_pack(const T* p) {
@@ -41,16 +40,57 @@ template <typename T, int V>
 MOE_DEVINL void store_pack(T* p, const Pack<T, V>& a) {
     *reinterpret_cast<Pack<T, V>*>(p) = a;
 }
-// V fp32 values rounded to T and stored (V * sizeof(T) may be 8, 16 or 32 bytes).
+
+MOE_DEVINL void unpack_word(float, uint32_t w, float* f) { f[0] = __uint_as_float(w); }
+MOE_DEVINL void unpack_word(__half, uint32_t w, float* f) {
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    f[0] = v.x;
+    f[1] = v.y;
+}
+MOE_DEVINL void unpack_word(__nv_bfloat16, uint32_t w, float* f) {
+    f[0] = bf16lo(w);
+    f[1] = bf16hi(w);
+}
+template <typename T, int V>
+MOE_DEVINL void unpack(const Pack<T, V>& a, float (&f)[V]) {
+    if constexpr (V * sizeof(T) == 2) {
+        float g[2];
+        unpack_word(T{}, a, g);
+        f[0] = g[0];
+    } else {
+        constexpr int N = V * (int)sizeof(T) / 4, PER = 4 / (int)sizeof(T);
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&a);
+#pragma unroll
+        for (int i = 0; i < N; ++i) unpack_word(T{}, w[i], f + i * PER);
+    }
+}
+
+MOE_DEVINL uint32_t pack_word(float, const float* f) { return __float_as_uint(f[0]); }
+MOE_DEVINL uint32_t pack_word(__half, const float* f) {
+    const __half2 h = __floats2half2_rn(f[0], f[1]);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+MOE_DEVINL uint32_t pack_word(__nv_bfloat16, const float* f) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f[0], f[1]);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// V fp32 values rounded to T and stored, or V elements loaded as fp32, in
+// accesses of at most 16 bytes (V fp32 values for V elements of 2 bytes are 32).
 template <typename T, int V>
 MOE_DEVINL void store_f32(T* p, const float (&f)[V]) {
-    constexpr int W = V * sizeof(T) > 16 ? 16 / (int)sizeof(T) : V;
+    if constexpr (V == 1) {
+        *p = from_f32<T>(f[0]);
+    } else {
+        constexpr int W = V * sizeof(T) > 16 ? 16 / (int)sizeof(T) : V, PER = 4 / (int)sizeof(T);
 #pragma unroll
-    for (int i = 0; i < V; i += W) {
-        Pack<T, W> a;
+        for (int i = 0; i < V; i += W) {
+            Pack<T, W> a;
+            uint32_t* w = reinterpret_cast<uint32_t*>(&a);
 #pragma unroll
-        for (int j = 0; j < W; ++j) a.v[j] = from_f32<T>(f[i + j]);
-        store_pack<T, W>(p + i, a);
+            for (int j = 0; j < W / PER; ++j) w[j] = pack_word(T{}, f + i + j * PER);
+            store_pack<T, W>(p + i, a);
+        }
     }
 }
 template <typename T, int V>
@@ -58,9 +98,21 @@ MOE_DEVINL void load_f32(const T* p, float (&f)[V]) {
     constexpr int W = V * sizeof(T) > 16 ? 16 / (int)sizeof(T) : V;
 #pragma unroll
     for (int i = 0; i < V; i += W) {
-        const Pack<T, W> a = load_pack<T, W>(p + i);
+        float g[W];
+        unpack<T, W>(load_pack<T, W>(p + i), g);
 #pragma unroll
-        for (int j = 0; j < W; ++j) f[i + j] = to_f32(a.v[j]);
+        for (int j = 0; j < W; ++j) f[i + j] = g[j];
+    }
+}
+// v as it reads back after a store as T
+template <typename T>
+MOE_DEVINL float as_stored(float v) {
+    if constexpr (sizeof(T) == 4) return v;
+    else {
+        const float f[2] = {v, 0.f};
+        float g[2];
+        unpack_word(T{}, pack_word(T{}, f), g);
+        return g[0];
     }
 }
 

@@ -307,10 +307,10 @@ def _dtype(name, t):
 
 
 def _arg(name, t, dtype, shape, device):
-    """The device address of a contiguous tensor of this type and shape (0 for None)."""
+    """The device address of a contiguous tensor of this type and shape (None for None)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, not "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', strided'}")
     return t.data_ptr()
@@ -321,11 +321,13 @@ def _call(fn, device, stream, *args):
         raise ValueError(f"{fn} takes CUDA tensors, not tensors on {device}")
     if stream is not None and stream.device != device:
         raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on {device}")
-    if device.index != torch.cuda.current_device():
+    index = device.index
+    if index != torch.cuda.current_device():
         with torch.cuda.device(device):
             return _call(fn, device, stream, *args)
-    handle = (torch.cuda.current_stream() if stream is None else stream).cuda_stream
-    st = getattr(lib(), fn)(*args, handle)
+    # the handle alone: torch.cuda.current_stream() makes a Stream object, 3 us of a decode step's call
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    st = getattr(_lib or lib(), fn)(*args, handle)
     if st != MOE_OK:
         raise MoeError(fn, st)
 
