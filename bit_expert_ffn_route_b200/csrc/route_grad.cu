@@ -19,11 +19,38 @@ namespace {
 using B16 = __nv_bfloat16;
 
 constexpr int kSliceThreads = 1024;
-constexpr int kSliceSmem = 200 * 1024;     // a slice of Wr: all experts, 128 columns (64 beyond 800 experts)
+constexpr int kSliceTile = 64;             // tokens whose pairs a slice block holds at a time, times k <= 16: a pair per thread
+constexpr int kSliceMaxE = 800;            // experts whose 128 columns fit in shared memory beside the pairs; 64 beyond
 constexpr int kDwThreads = 128;            // columns of dWr per block: 8 per thread
 constexpr int kDwChunks = 1280;            // chunks of pairs that the dWr sums are cut into, about
 constexpr int kDwDepth = 8;                // rows of x in flight per thread
 constexpr int kDwMaxChunk = 1024;
+constexpr int kJoinWarps = 8;
+
+// Eight fp32 sums as four pairs: fma.rn.f32x2 makes two multiply-adds, each
+// rounded as fmaf rounds it.
+struct Sum8 {
+    unsigned long long v[4] = {0, 0, 0, 0};     // +0, +0
+    MOE_DEVINL void add(float d, const Pack<B16, 8>& a) {
+        unsigned long long m;
+        asm("mov.b64 %0, {%1, %1};" : "=l"(m) : "f"(d));
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&a);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            unsigned long long x;
+            asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(bf16lo(w[i])), "f"(bf16hi(w[i])));
+            asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(v[i]) : "l"(m), "l"(x));
+        }
+    }
+    MOE_DEVINL void get(float (&f)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm("mov.b64 {%0, %1}, %2;" : "=f"(f[2 * i]), "=f"(f[2 * i + 1]) : "l"(v[i]));
+    }
+    MOE_DEVINL void set(const float (&f)[8]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm("mov.b64 %0, {%1, %2};" : "=l"(v[i]) : "f"(f[2 * i]), "f"(f[2 * i + 1]));
+    }
+};
 
 // Lane r < k: the gradient of the token's r-th selected logit, and its expert
 // (-1: id outside [0, E), gradient 0).
@@ -46,6 +73,7 @@ __global__ void __launch_bounds__(256) route_dlogits_kernel(const float* __restr
                                                             const int32_t* __restrict__ ids, int T, int E, int k,
                                                             float* __restrict__ dlogits) {
     pdl_wait();
+    pdl_launch_dependents();
     const int t = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (t >= T) return;
     int id;
@@ -73,63 +101,105 @@ __global__ void __launch_bounds__(128) route_dx_kernel(const float* __restrict__
         e[r] = __shfl_sync(0xffffffffu, id, r);
         if (e[r] >= 0 && c < D) w[r] = load_pack<B16, 8>(Wr + (size_t)e[r] * D + c);
     }
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (dx_add && c < D) load_f32<B16, 8>(dx_add + t * D + c, acc);
+    Sum8 sum;
+    float acc[8];
+    if (dx_add && c < D) {
+        load_f32<B16, 8>(dx_add + t * D + c, acc);
+        sum.set(acc);
+    }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const float d = __shfl_sync(0xffffffffu, dl, r);
-        if (e[r] < 0 || c >= D) continue;
-        float v[8];
-        unpack<B16, 8>(w[r], v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = __fmaf_rn(d, v[i], acc[i]);
+        if (e[r] >= 0 && c < D) sum.add(d, w[r]);
     }
+    sum.get(acc);
     if (c < D) store_f32<B16, 8>(dx + t * D + c, acc);
 }
 
-// Many tokens: block (slice, group) keeps 32 N columns of all experts' rows in
-// shared memory and its warps walk over the group's tokens, one row of the
-// slice per pair.
-template <int N>
-__global__ void __launch_bounds__(kSliceThreads) route_dx_slice_kernel(const float* __restrict__ dgates,
-                                                                       const float* __restrict__ gates,
-                                                                       const int32_t* __restrict__ ids,
-                                                                       const B16* __restrict__ Wr, int T, int D, int E,
-                                                                       int k, const B16* dx_add,
-                                                                       float* __restrict__ dlogits, B16* dx) {
-    extern __shared__ __align__(16) B16 slice[];        // [E][32 N]
-    constexpr int W = 32 * N, kCopies = W * 2 / 16;     // 16-byte copies per expert
-    const int lane = threadIdx.x & 31, c = blockIdx.x * W;
-    pdl_wait();
+// Many tokens: block (slice, group) keeps W = 256 / G columns of all experts'
+// rows in shared memory and walks over the group's tokens, 64 at a time.  A warp
+// takes a token: G groups of lanes each add up every G-th pair over all W columns
+// (16 bytes per lane, S steps), then exchange halves so that a lane ends with
+// 8 / G columns.  Shared memory reads each pair's row once, at 128 bytes per
+// clock; the instructions (unpacking, two multiply-adds each) are the larger
+// part.  The row past the last expert is zero: pairs without expert, and the pairs
+// that round k up to S G, point there.
+template <int G, int S>
+__global__ void __launch_bounds__(kSliceThreads, 1) route_dx_slice_kernel(const float* __restrict__ dlogits,
+                                                                          const int32_t* __restrict__ ids,
+                                                                          const B16* __restrict__ Wr, int T, int D,
+                                                                          int E, int k, const B16* dx_add, B16* dx) {
+    extern __shared__ __align__(16) B16 slice[];        // [E + 1][W], then the tile's pairs, twice
+    constexpr int W = 256 / G, kCopies = W * 2 / 16, L = 32 / G;
+    constexpr int S2 = (S + 1) / 2 * 2, kPairs = G * S2;    // a group's pairs of a token, read two at a time
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * W;
+    int2* pairs = reinterpret_cast<int2*>(slice + (size_t)(E + 1) * W);
+    // Wr was complete before the kernel in front of this one began
     for (int i = threadIdx.x; i < E * kCopies; i += kSliceThreads) {
         const int e = i / kCopies, j = i % kCopies * 8;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(slice + e * W + j)),
                      "l"(Wr + (size_t)e * D + c + j)
                      : "memory");
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncthreads();
-    const int step = gridDim.y * (kSliceThreads / 32);
-    for (int t = blockIdx.y * (kSliceThreads / 32) + (threadIdx.x >> 5); t < T; t += step) {
-        int id;
-        const float dl = token_dlogit(dgates, gates, ids, t, k, E, lane, id);
-        if (blockIdx.x == 0 && lane < k) dlogits[(size_t)t * k + lane] = dl;
-        const size_t at = (size_t)t * D + c + lane * N;
-        float acc[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] = 0.f;
-        if (dx_add) load_f32<B16, N>(dx_add + at, acc);
-#pragma unroll 4
-        for (int r = 0; r < k; ++r) {
-            const int e = __shfl_sync(0xffffffffu, id, r);
-            const float d = __shfl_sync(0xffffffffu, dl, r);
-            if (e < 0) continue;
-            float v[N];
-            load_f32<B16, N>(slice + e * W + lane * N, v);
-#pragma unroll
-            for (int i = 0; i < N; ++i) acc[i] = __fmaf_rn(d, v[i], acc[i]);
+    for (int i = threadIdx.x; i < W; i += kSliceThreads) slice[E * W + i] = from_f32<B16>(0.f);
+    pdl_wait();
+    // thread: the pair (token of the tile, rank) that it fetches for every tile
+    const int my_tok = threadIdx.x / kPairs, my_r = threadIdx.x % S2 * G + threadIdx.x % kPairs / S2;
+    const bool mine = my_tok < kSliceTile, real = mine && threadIdx.x % S2 < S && my_r < k;
+    const int step = gridDim.y * kSliceTile;
+    auto fetch = [&](int t0) {
+        int2 q = {E * W, 0};
+        if (real && t0 + my_tok < T) {
+            const size_t p = (size_t)(t0 + my_tok) * k + my_r;
+            const int e = __ldg(ids + p);
+            const float dl = __ldg(dlogits + p);
+            if (e >= 0 && e < E) q = {e * W, __float_as_int(dl)};
         }
-        store_f32<B16, N>(dx + at, acc);
+        return q;
+    };
+    int2 next = fetch(blockIdx.y * kSliceTile);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    int buf = 0;
+    for (int t0 = blockIdx.y * kSliceTile; t0 < T; t0 += step, buf ^= 1) {
+        int2* tile = pairs + buf * kSliceTile * kMaxTopK;
+        if (mine) tile[threadIdx.x] = next;
+        __syncthreads();                                // two buffers: the tile before last is done with by all
+        next = fetch(t0 + step);
+        const B16* col = slice + lane % L * 8;
+        for (int i = warp; i < kSliceTile && t0 + i < T; i += kSliceThreads / 32) {
+            const int4* q = reinterpret_cast<const int4*>(tile + i * kPairs + lane / L * S2);
+            Sum8 sum;
+#pragma unroll
+            for (int s = 0; s < S; s += 2) {
+                const int4 v = q[s / 2];
+                sum.add(__int_as_float(v.y), load_pack<B16, 8>(col + v.x));
+                if (s + 1 < S) sum.add(__int_as_float(v.w), load_pack<B16, 8>(col + v.z));
+            }
+            float acc[8];
+            sum.get(acc);
+            int at = lane % L * 8;
+#pragma unroll
+            for (int n = 4, bit = 16; n * G >= 8; n /= 2, bit /= 2) {
+                const bool up = lane & bit;
+#pragma unroll
+                for (int j = 0; j < n; ++j) {
+                    const float give = up ? acc[j] : acc[j + n], keep = up ? acc[j + n] : acc[j];
+                    acc[j] = keep + __shfl_xor_sync(0xffffffffu, give, bit);
+                }
+                at += up ? n : 0;
+            }
+            float out[8 / G];
+            const size_t to = (size_t)(t0 + i) * D + c + at;
+#pragma unroll
+            for (int j = 0; j < 8 / G; ++j) out[j] = acc[j];
+            if (dx_add) {
+                float add[8 / G];
+                load_f32<B16, 8 / G>(dx_add + to, add);
+#pragma unroll
+                for (int j = 0; j < 8 / G; ++j) out[j] += add[j];
+            }
+            store_f32<B16, 8 / G>(dx + to, out);
+        }
     }
 }
 
@@ -146,98 +216,117 @@ __global__ void __launch_bounds__(kDwThreads) route_dw_kernel(const float* __res
                                                               const int32_t* __restrict__ row_pair, int P, int D, int E,
                                                               int k, int chunk, float* __restrict__ dWr,
                                                               float* __restrict__ part) {
-    __shared__ int s_tok[kDwMaxChunk], s_exp[kDwMaxChunk];
-    __shared__ float s_dl[kDwMaxChunk];
+    // of every row: the offset of its token in x, with bit 0 set where an expert begins, and dl
+    __shared__ uint2 s_row[kDwMaxChunk];
+    __shared__ int s_exp[kDwMaxChunk];
     pdl_wait();
     const int j0 = blockIdx.x * chunk;
     const int n = min(chunk, min(P, __ldg(offsets + E)) - j0);
-    if (n <= 0) return;
-    for (int j = threadIdx.x; j < n; j += kDwThreads) {
-        const int p = __ldg(row_pair + j0 + j);
+    for (int j = threadIdx.x; j < min(chunk, P - j0); j += kDwThreads) {
+        const int p = __ldg(row_pair + j0 + j);     // anything beyond the plan's rows
         int e = -1;
-        if (p >= 0 && p < P) e = __ldg(ids + p);
+        float dl = 0.f;
+        if (p >= 0 && p < P) {
+            e = __ldg(ids + p);
+            dl = __ldg(dlogits + p);
+        }
         if (e < 0 || e >= E) e = -1;            // not what a plan of these ids holds
         s_exp[j] = e;
-        s_tok[j] = e >= 0 ? p / k : 0;
-        s_dl[j] = e >= 0 ? __ldg(dlogits + p) : 0.f;
+        s_row[j] = e >= 0 ? make_uint2((uint32_t)(p / k) * (uint32_t)D, __float_as_uint(dl)) : make_uint2(0u, 0u);
     }
+    if (n <= 0) return;
+    __syncthreads();
+    for (int j = threadIdx.x; j < n; j += kDwThreads)
+        if (j > 0 && s_exp[j] != s_exp[j - 1]) s_row[j].x |= 1u;
     __syncthreads();
     const int c = (blockIdx.y * kDwThreads + threadIdx.x) * 8;
     if (c >= D) return;
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    Sum8 sum;
     auto flush = [&](int e) {
+        float acc[8];
+        sum.get(acc);
+        sum = Sum8();
         if (e < 0) return;
         float* to = dWr + (size_t)e * D;
         if (__ldg(offsets + e) < j0) to = part + (size_t)(2 * blockIdx.x) * D;
         else if (__ldg(offsets + e + 1) > j0 + n) to = part + (size_t)(2 * blockIdx.x + 1) * D;
         store_f32<float, 8>(to + c, acc);
     };
-    int cur = s_exp[0];
-    for (int j = 0; j < n; j += kDwDepth) {
+    const B16* xc = x + c;
+    int j = 0;
+    for (; j + kDwDepth <= n; j += kDwDepth) {
         Pack<B16, 8> a[kDwDepth];
-#pragma unroll
-        for (int i = 0; i < kDwDepth; ++i)
-            if (j + i < n) a[i] = load_pack<B16, 8>(x + (size_t)s_tok[j + i] * D + c);
+        uint2 row[kDwDepth];
 #pragma unroll
         for (int i = 0; i < kDwDepth; ++i) {
-            if (j + i >= n) break;
-            if (s_exp[j + i] != cur) {
-                flush(cur);
-                cur = s_exp[j + i];
+            row[i] = s_row[j + i];
+            a[i] = load_pack<B16, 8>(xc + (row[i].x & ~1u));
+        }
 #pragma unroll
-                for (int q = 0; q < 8; ++q) acc[q] = 0.f;
-            }
-            const float dl = s_dl[j + i];
-            float v[8];
-            unpack<B16, 8>(a[i], v);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) acc[q] = __fmaf_rn(dl, v[q], acc[q]);
+        for (int i = 0; i < kDwDepth; ++i) {
+            if (row[i].x & 1u) flush(s_exp[j + i - 1]);
+            sum.add(__uint_as_float(row[i].y), a[i]);
         }
     }
-    flush(cur);
+    for (; j < n; ++j) {
+        const uint2 row = s_row[j];
+        if (row.x & 1u) flush(s_exp[j - 1]);
+        sum.add(__uint_as_float(row.y), load_pack<B16, 8>(xc + (row.x & ~1u)));
+    }
+    flush(s_exp[n - 1]);
 }
 
-// Block (e, columns): the sums of an expert whose rows lie in several chunks, a
-// zero row for an expert without any, and dbias.
-__global__ void __launch_bounds__(kDwThreads) route_join_kernel(const float* __restrict__ dlogits,
-                                                                const int32_t* __restrict__ offsets,
-                                                                const int32_t* __restrict__ row_pair, int P, int D,
-                                                                int chunk, const float* __restrict__ part,
-                                                                float* __restrict__ dWr, float* __restrict__ dbias) {
-    __shared__ float wsum[kDwThreads / 32];
+// Block (e, 256 columns): the sums of an expert whose rows lie in several chunks
+// (a warp adds up an eighth of them, then the eighths in order), and a zero row
+// for an expert without any; the last block of an expert sums dbias.
+__global__ void __launch_bounds__(kJoinWarps * 32) route_join_kernel(const float* __restrict__ dlogits,
+                                                                     const int32_t* __restrict__ offsets,
+                                                                     const int32_t* __restrict__ row_pair, int P, int D,
+                                                                     int chunk, const float* __restrict__ part,
+                                                                     float* __restrict__ dWr,
+                                                                     float* __restrict__ dbias) {
+    __shared__ float sums[kJoinWarps][256];
     pdl_wait();
-    const int e = blockIdx.x;
+    const int e = blockIdx.x, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int r0 = max(0, __ldg(offsets + e)), r1 = min(P, __ldg(offsets + e + 1));
-    if (dbias && blockIdx.y == 0) {
+    if (blockIdx.y == gridDim.y - 1) {
+        if (!dbias) return;
         float s = 0.f;
-        for (int j = r0 + threadIdx.x; j < r1; j += kDwThreads) {
+#pragma unroll 4
+        for (int j = r0 + threadIdx.x; j < r1; j += kJoinWarps * 32) {
             const int p = __ldg(row_pair + j);
-            if (p >= 0 && p < P) s += __ldg(dlogits + p);
+            s += p >= 0 && p < P ? __ldg(dlogits + p) : 0.f;
         }
         s = warp_sum(s);
-        if ((threadIdx.x & 31) == 0) wsum[threadIdx.x >> 5] = s;
+        if (lane == 0) sums[0][w] = s;
         __syncthreads();
         if (threadIdx.x == 0) {
-            for (int i = 1; i < kDwThreads / 32; ++i) s += wsum[i];
+            for (int i = 1; i < kJoinWarps; ++i) s += sums[0][i];
             dbias[e] = s;
         }
+        return;
     }
-    const int c = (blockIdx.y * kDwThreads + threadIdx.x) * 8;
-    if (!dWr || c >= D) return;
     const int a = r0 / chunk, b = (r1 - 1) / chunk;
     if (r1 > r0 && a == b) return;              // stored by its block
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const int c = blockIdx.y * 256;
     if (r1 > r0) {
-        load_f32<float, 8>(part + (size_t)(2 * a + 1) * D + c, acc);
+        // partial a is the expert's beginning (odd slot), the others' rows go on from the chunk before
+        const int each = (b - a + kJoinWarps) / kJoinWarps, i0 = a + w * each, i1 = min(b + 1, i0 + each);
 #pragma unroll 4
-        for (int i = a + 1; i <= b; ++i) {
+        for (int i = i0; i < i1; ++i) {
             float v[8];
-            load_f32<float, 8>(part + (size_t)(2 * i) * D + c, v);
+            load_f32<float, 8>(part + (size_t)(2 * i + (i == a)) * D + c + lane * 8, v);
 #pragma unroll
             for (int q = 0; q < 8; ++q) acc[q] += v[q];
         }
     }
-    store_f32<float, 8>(dWr + (size_t)e * D + c, acc);
+    store_f32<float, 8>(&sums[w][lane * 8], acc);
+    __syncthreads();
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kJoinWarps; ++i) s += sums[i][threadIdx.x];
+    dWr[(size_t)e * D + c + threadIdx.x] = s;
 }
 
 // Rows per chunk: a multiple of 16.
@@ -259,14 +348,31 @@ size_t route_grad_ws_bytes(int T, int D, int k) {
     return 256 + (size_t)2 * ((P + chunk - 1) / chunk) * D * 4;
 }
 
+size_t slice_smem(int E, int G) {
+    return (size_t)(E + 1) * (256 / G) * 2 + (size_t)2 * kSliceTile * kMaxTopK * sizeof(int2);
+}
+
+template <int G, int S>
+cudaError_t slice_steps(const float* dlogits, const int32_t* ids, const B16* Wr, int T, int D, int E, int k, int groups,
+                        const B16* dx_add, B16* dx, cudaStream_t s) {
+    static std::atomic<uint64_t> set{0};
+    if (!once_per_device(set, [] {
+            return cudaFuncSetAttribute(route_dx_slice_kernel<G, S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        (int)slice_smem(G == 2 ? kSliceMaxE : kOpsMaxE, G)) == cudaSuccess;
+        }))
+        return cudaErrorUnknown;
+    return launch_pdl(route_dx_slice_kernel<G, S>, dim3(D / (256 / G), groups), dim3(kSliceThreads), slice_smem(E, G), s,
+                      dlogits, ids, Wr, T, D, E, k, dx_add, dx);
+}
+
 cudaError_t launch_dx(const float* dgates, const float* gates, const int32_t* ids, const B16* Wr, int T, int D, int E,
                       int k, const B16* dx_add, float* dlogits, B16* dx, cudaStream_t s) {
-    if (!dx) return launch_pdl(route_dlogits_kernel, dim3((T + 7) / 8), dim3(256), 0, s, dgates, gates, ids, T, E, k, dlogits);
     // A slice block reads its columns of all E rows once, the direct kernel one row per pair: the slices' reads are
     // `groups` times Wr.
-    const int N = E * 256 <= kSliceSmem ? 4 : 2, slices = D / (32 * N);
+    const int G = E <= kSliceMaxE ? 2 : 4, slices = D / (256 / G);
     const int groups = slices < device_sm_count() ? device_sm_count() / slices : 1;
-    if ((long long)T * k < 2ll * groups * E) {
+    const bool sliced = dx && (long long)T * k >= 2ll * groups * E;
+    if (dx && !sliced) {
         auto go = [&](auto kernel) {
             return launch_pdl(kernel, dim3(T, (D + 1023) / 1024), dim3(128), 0, s, dgates, gates, ids, Wr, D, E, k, dx_add,
                               dlogits, dx);
@@ -276,17 +382,23 @@ cudaError_t launch_dx(const float* dgates, const float* gates, const int32_t* id
         if (k <= 12) return go(route_dx_kernel<12>);
         return go(route_dx_kernel<16>);
     }
-    static std::atomic<uint64_t> set{0};
-    if (!once_per_device(set, [] {
-            return cudaFuncSetAttribute(route_dx_slice_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        kSliceSmem) == cudaSuccess &&
-                   cudaFuncSetAttribute(route_dx_slice_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        kSliceSmem) == cudaSuccess;
-        }))
-        return cudaErrorUnknown;
-    auto kernel = N == 4 ? route_dx_slice_kernel<4> : route_dx_slice_kernel<2>;
-    return launch_pdl(kernel, dim3(slices, groups), dim3(kSliceThreads), (size_t)E * 64 * N, s, dgates, gates, ids, Wr, T,
-                      D, E, k, dx_add, dlogits, dx);
+    cudaError_t e = launch_pdl(route_dlogits_kernel, dim3((T + 7) / 8), dim3(256), 0, s, dgates, gates, ids, T, E, k,
+                               dlogits);
+    if (!sliced || e != cudaSuccess) return e;
+    if (G == 4) return k <= 4 ? slice_steps<4, 1>(dlogits, ids, Wr, T, D, E, k, groups, dx_add, dx, s)
+                     : k <= 8 ? slice_steps<4, 2>(dlogits, ids, Wr, T, D, E, k, groups, dx_add, dx, s)
+                     : k <= 12 ? slice_steps<4, 3>(dlogits, ids, Wr, T, D, E, k, groups, dx_add, dx, s)
+                               : slice_steps<4, 4>(dlogits, ids, Wr, T, D, E, k, groups, dx_add, dx, s);
+    switch ((k + 1) / 2) {
+        case 1: return slice_steps<2, 1>(dlogits, ids, Wr, T, D, E, k, groups, dx_add, dx, s);
+        case 2: return slice_steps<2, 2>(dlogits, ids, Wr, T, D, E, k, groups, dx_add, dx, s);
+        case 3: return slice_steps<2, 3>(dlogits, ids, Wr, T, D, E, k, groups, dx_add, dx, s);
+        case 4: return slice_steps<2, 4>(dlogits, ids, Wr, T, D, E, k, groups, dx_add, dx, s);
+        case 5: return slice_steps<2, 5>(dlogits, ids, Wr, T, D, E, k, groups, dx_add, dx, s);
+        case 6: return slice_steps<2, 6>(dlogits, ids, Wr, T, D, E, k, groups, dx_add, dx, s);
+        case 7: return slice_steps<2, 7>(dlogits, ids, Wr, T, D, E, k, groups, dx_add, dx, s);
+        default: return slice_steps<2, 8>(dlogits, ids, Wr, T, D, E, k, groups, dx_add, dx, s);
+    }
 }
 
 }  // namespace
@@ -326,12 +438,14 @@ extern "C" moe_status moe_route_backward(const float* dgates, const float* gates
     cudaError_t e = launch_dx(dgates, gates, ids, Wb, T, D, E, k, reinterpret_cast<const B16*>(dx_add), dlogits,
                               reinterpret_cast<B16*>(dx), s);
     if (e != cudaSuccess || (!dWr && !dbias)) return ops_status(e);
-    const int P = T * k, chunk = dw_chunk(P), cols = dWr ? (D + kDwThreads * 8 - 1) / (kDwThreads * 8) : 1;
+    const int P = T * k, chunk = dw_chunk(P);
     float* part = static_cast<float*>(ws);
     if (dWr)
-        e = launch_pdl(route_dw_kernel, dim3((P + chunk - 1) / chunk, cols), dim3(kDwThreads), 0, s,
-                       (const float*)dlogits, ids, xb, offsets, row_pair, P, D, E, k, chunk, dWr, part);
+        e = launch_pdl(route_dw_kernel, dim3((P + chunk - 1) / chunk, (D + kDwThreads * 8 - 1) / (kDwThreads * 8)),
+                       dim3(kDwThreads), 0, s, (const float*)dlogits, ids, xb, offsets, row_pair, P, D, E, k, chunk, dWr,
+                       part);
     if (e != cudaSuccess) return ops_status(e);
-    return ops_status(launch_pdl(route_join_kernel, dim3(E, cols), dim3(kDwThreads), 0, s, (const float*)dlogits,
-                                 offsets, row_pair, P, D, chunk, (const float*)part, dWr, dbias));
+    return ops_status(launch_pdl(route_join_kernel, dim3(E, (dWr ? D / 256 : 0) + 1), dim3(kJoinWarps * 32), 0, s,
+                                 (const float*)dlogits, offsets, row_pair, P, D, chunk, (const float*)part, dWr,
+                                 dbias));
 }
