@@ -22,10 +22,11 @@ constexpr int kSliceThreads = 1024;
 constexpr int kSliceTile = 64;             // tokens whose pairs a slice block holds at a time, times k <= 16: a pair per thread
 constexpr int kSliceMaxE = 800;            // experts whose 128 columns fit in shared memory beside the pairs; 64 beyond
 constexpr int kDwThreads = 128;            // columns of dWr per block: 8 per thread
-constexpr int kDwChunks = 1280;            // chunks of pairs that the dWr sums are cut into, about
-constexpr int kDwDepth = 8;                // rows of x in flight per thread
-constexpr int kDwMaxChunk = 1024;
-constexpr int kJoinWarps = 8;
+constexpr int kDwChunks = 320;            // chunks of pairs that the dWr sums are cut into, about
+constexpr int kDwDepth = 4;                // rows of x in flight per thread
+constexpr int kJoinThreads = 256;
+constexpr int kJoinParts = 4;              // shares of an expert's partial sums, added up at the same time
+constexpr int kJoinCols = kJoinThreads / kJoinParts * 8;
 
 // Eight fp32 sums as four pairs: fma.rn.f32x2 makes two multiply-adds, each
 // rounded as fmaf rounds it.
@@ -217,8 +218,8 @@ __global__ void __launch_bounds__(kDwThreads) route_dw_kernel(const float* __res
                                                               int k, int chunk, float* __restrict__ dWr,
                                                               float* __restrict__ part) {
     // of every row: the offset of its token in x, with bit 0 set where an expert begins, and dl
-    __shared__ uint2 s_row[kDwMaxChunk];
-    __shared__ int s_exp[kDwMaxChunk];
+    extern __shared__ uint2 s_row[];
+    int* s_exp = reinterpret_cast<int*>(s_row + chunk);
     pdl_wait();
     const int j0 = blockIdx.x * chunk;
     const int n = min(chunk, min(P, __ldg(offsets + E)) - j0);
@@ -276,57 +277,63 @@ __global__ void __launch_bounds__(kDwThreads) route_dw_kernel(const float* __res
     flush(s_exp[n - 1]);
 }
 
-// Block (e, 256 columns): the sums of an expert whose rows lie in several chunks
-// (a warp adds up an eighth of them, then the eighths in order), and a zero row
-// for an expert without any; the last block of an expert sums dbias.
-__global__ void __launch_bounds__(kJoinWarps * 32) route_join_kernel(const float* __restrict__ dlogits,
-                                                                     const int32_t* __restrict__ offsets,
-                                                                     const int32_t* __restrict__ row_pair, int P, int D,
-                                                                     int chunk, const float* __restrict__ part,
-                                                                     float* __restrict__ dWr,
-                                                                     float* __restrict__ dbias) {
-    __shared__ float sums[kJoinWarps][256];
+// Block (e, 512 columns): the sums of an expert whose rows lie in several chunks
+// (a quarter of the threads adds up a quarter of them, then the quarters in
+// order), and a zero row for an expert without any; the last block of an expert
+// sums dbias.
+__global__ void __launch_bounds__(kJoinThreads) route_join_kernel(const float* __restrict__ dlogits,
+                                                                  const int32_t* __restrict__ offsets,
+                                                                  const int32_t* __restrict__ row_pair, int P, int D,
+                                                                  int chunk, const float* __restrict__ part,
+                                                                  float* __restrict__ dWr, float* __restrict__ dbias) {
+    __shared__ float sums[kJoinParts][kJoinCols];
     pdl_wait();
-    const int e = blockIdx.x, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int e = blockIdx.x;
     const int r0 = max(0, __ldg(offsets + e)), r1 = min(P, __ldg(offsets + e + 1));
     if (blockIdx.y == gridDim.y - 1) {
         if (!dbias) return;
         float s = 0.f;
 #pragma unroll 4
-        for (int j = r0 + threadIdx.x; j < r1; j += kJoinWarps * 32) {
+        for (int j = r0 + threadIdx.x; j < r1; j += kJoinThreads) {
             const int p = __ldg(row_pair + j);
             s += p >= 0 && p < P ? __ldg(dlogits + p) : 0.f;
         }
         s = warp_sum(s);
-        if (lane == 0) sums[0][w] = s;
+        if (threadIdx.x % 32 == 0) sums[0][threadIdx.x / 32] = s;
         __syncthreads();
         if (threadIdx.x == 0) {
-            for (int i = 1; i < kJoinWarps; ++i) s += sums[0][i];
+            for (int i = 1; i < kJoinThreads / 32; ++i) s += sums[0][i];
             dbias[e] = s;
         }
         return;
     }
     const int a = r0 / chunk, b = (r1 - 1) / chunk;
     if (r1 > r0 && a == b) return;              // stored by its block
+    const int g = threadIdx.x / (kJoinCols / 8), col = threadIdx.x % (kJoinCols / 8) * 8;
+    const int c = blockIdx.y * kJoinCols;
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    const int c = blockIdx.y * 256;
-    if (r1 > r0) {
+    if (r1 > r0 && c + col < D) {
         // partial a is the expert's beginning (odd slot), the others' rows go on from the chunk before
-        const int each = (b - a + kJoinWarps) / kJoinWarps, i0 = a + w * each, i1 = min(b + 1, i0 + each);
+        const int each = (b - a + kJoinParts) / kJoinParts, i0 = a + g * each, i1 = min(b + 1, i0 + each);
 #pragma unroll 4
         for (int i = i0; i < i1; ++i) {
             float v[8];
-            load_f32<float, 8>(part + (size_t)(2 * i + (i == a)) * D + c + lane * 8, v);
+            load_f32<float, 8>(part + (size_t)(2 * i + (i == a)) * D + c + col, v);
 #pragma unroll
             for (int q = 0; q < 8; ++q) acc[q] += v[q];
         }
     }
-    store_f32<float, 8>(&sums[w][lane * 8], acc);
+    store_f32<float, 8>(&sums[g][col], acc);
     __syncthreads();
-    float s = 0.f;
+    for (int i = threadIdx.x * 2; i < kJoinCols && c + i < D; i += kJoinThreads * 2) {
+        float s[2] = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < kJoinWarps; ++i) s += sums[i][threadIdx.x];
-    dWr[(size_t)e * D + c + threadIdx.x] = s;
+        for (int j = 0; j < kJoinParts; ++j) {
+            s[0] += sums[j][i];
+            s[1] += sums[j][i + 1];
+        }
+        store_f32<float, 2>(dWr + (size_t)e * D + c + i, s);
+    }
 }
 
 // Rows per chunk: a multiple of 16.
@@ -442,10 +449,10 @@ extern "C" moe_status moe_route_backward(const float* dgates, const float* gates
     float* part = static_cast<float*>(ws);
     if (dWr)
         e = launch_pdl(route_dw_kernel, dim3((P + chunk - 1) / chunk, (D + kDwThreads * 8 - 1) / (kDwThreads * 8)),
-                       dim3(kDwThreads), 0, s, (const float*)dlogits, ids, xb, offsets, row_pair, P, D, E, k, chunk, dWr,
+                       dim3(kDwThreads), (size_t)chunk * (sizeof(uint2) + sizeof(int)), s, (const float*)dlogits, ids, xb, offsets, row_pair, P, D, E, k, chunk, dWr,
                        part);
     if (e != cudaSuccess) return ops_status(e);
-    return ops_status(launch_pdl(route_join_kernel, dim3(E, (dWr ? D / 256 : 0) + 1), dim3(kJoinWarps * 32), 0, s,
+    return ops_status(launch_pdl(route_join_kernel, dim3(E, (dWr ? (D + kJoinCols - 1) / kJoinCols : 0) + 1), dim3(kJoinThreads), 0, s,
                                  (const float*)dlogits, offsets, row_pair, P, D, chunk, (const float*)part, dWr,
                                  dbias));
 }
