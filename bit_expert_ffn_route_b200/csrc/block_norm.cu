@@ -3,7 +3,14 @@
 //   z = y r_y w_post,  x_out = alpha residual + gate z,  normed = x_out r_x w_next,
 //   r = rsqrt(mean(v^2) + eps)
 // Each element of y and the residual is read once and each of x_out and normed
-// written once; a token stays in its block's registers between the two norms.
+// written once; a token stays in registers between the two norms.  Gradients
+// likewise: four rows in, two out.  HBM bounds both.
+//
+// Threads: a group of whole warps takes a token, each thread the same columns of
+// every token it takes, so that the sums over tokens stay in its registers;
+// short rows put several groups in a block.  Groups walk over the tokens and
+// fetch the rows of their next tokens with cp.async while they work: a thread
+// copies just what it will read itself, so no barrier guards the copies.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -14,18 +21,85 @@
 namespace moe {
 namespace {
 
-constexpr int kNormParts = 296;        // blocks of the backward pass, each with a partial of every weight gradient
+constexpr int kNormParts = 296;        // most blocks of the backward pass: two per SM, a partial of each weight gradient from every one
+constexpr int kNormThreads = 384;      // threads that the groups of a block fill, about
+constexpr int kMaxDynamic = 227 * 1024;
+constexpr int kMaxGroups = 12;         // named barriers 1..12
 
-// Sum of v over the block's threads, the same value in every thread; fixed
-// order (lanes, then warps).  `buf` is 32 floats used by this call only until
-// the next __syncthreads.
-MOE_DEVINL float block_sum(float v, float* buf) {
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    v = warp_sum(v);
-    if (lane == 0) buf[w] = v;
-    __syncthreads();
-    return warp_sum(lane < nw ? buf[lane] : 0.f);
+template <int N>
+MOE_DEVINL void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+MOE_DEVINL void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+MOE_DEVINL void cp_async16(void* to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
 }
+
+// A group's threads: rank in the group, its warps, and sums over them.
+struct Group {
+    int g, rank, size;                          // group in the block, thread in the group, threads per group
+    MOE_DEVINL explicit Group(int threads) : g(threadIdx.x / threads), rank(threadIdx.x % threads), size(threads) {}
+    // N sums over the group, the same bits in every thread: lanes, then warps, in
+    // a fixed order.  buf: [2][N][32] floats of this group; parity alternates
+    // from call to call, so one barrier per call is enough.
+    template <int N>
+    MOE_DEVINL void sum(float (&v)[N], float* buf, int parity) const {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+        if (size == 32) return;
+        float* b = buf + parity * N * 32;
+        if (lane == 0) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) b[i * 32 + rank / 32] = v[i];
+        }
+        asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(size) : "memory");
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = warp_sum(lane < size / 32 ? b[i * 32 + lane] : 0.f);
+    }
+};
+
+// The rows of a group's coming tokens: STAGES tokens ahead in shared memory
+// (16-byte packs), or read when they are wanted (STAGES 0).
+template <typename T, int V, int ITER, int ROWS, int STAGES>
+struct Rows {
+    const T* src[ROWS];                         // null: no such row
+    T* ring;                                    // [STAGES][ROWS][D] of this group
+    int D, rank, size, stage = 0;
+    MOE_DEVINL void fetch(int t, int T_, int to) {
+        if constexpr (STAGES > 0) {
+            if (t < T_) {
+#pragma unroll
+                for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+                    for (int i = 0; i < ITER; ++i) {
+                        const int c = (i * size + rank) * V;
+                        if (src[r] && c < D) cp_async16(ring + (size_t)(to * ROWS + r) * D + c, src[r] + (size_t)t * D + c);
+                    }
+            }
+            cp_async_commit();
+        }
+    }
+    MOE_DEVINL void begin(int t0, int step, int T_) {
+        if constexpr (STAGES > 0) {
+#pragma unroll
+            for (int i = 0; i < STAGES; ++i) fetch(t0 + i * step, T_, i);
+        }
+    }
+    MOE_DEVINL void wait() const {
+        if constexpr (STAGES > 0) cp_async_wait<STAGES - 1>();
+    }
+    MOE_DEVINL void read(int r, int i, int t, float (&v)[V]) const {
+        const int c = (i * size + rank) * V;
+        if constexpr (STAGES > 0) load_f32<T, V>(ring + (size_t)(stage * ROWS + r) * D + c, v);
+        else load_f32<T, V>(src[r] + (size_t)t * D + c, v);
+    }
+    // The token's rows have been read and used: fetch those of a later one in their place.
+    MOE_DEVINL void refill(int t, int step, int T_) {
+        if constexpr (STAGES > 0) {
+            fetch(t + STAGES * step, T_, stage);
+            stage = stage + 1 == STAGES ? 0 : stage + 1;
+        }
+    }
+};
 
 struct NormArgs {
     const void *y, *residual;
@@ -34,241 +108,381 @@ struct NormArgs {
     float alpha;
     const float *w_post, *w_next;
     float eps;
-    int D;
+    int T, D, group;                            // group: threads per token
     void *x_out, *normed;
     float *rstd_post, *rstd_next;
 };
 
-// One block per token, ITER packs of V elements per thread.
-template <typename T, int V, int ITER>
-__global__ void __launch_bounds__(1024) block_norm_kernel(NormArgs a) {
-    __shared__ float buf[2][32];
+template <typename T, int V, int ITER, int STAGES, int THREADS>
+__global__ void __launch_bounds__(THREADS) block_norm_kernel(NormArgs a) {
+    extern __shared__ __align__(16) float dyn[];        // of every group: [2][32] for its sums; its ring
+    const Group grp(a.group);
+    const int groups = blockDim.x / a.group, step = gridDim.x * groups, t0 = blockIdx.x * groups + grp.g;
+    Rows<T, V, ITER, 2, STAGES> in;
+    in.src[0] = static_cast<const T*>(a.y);
+    in.src[1] = static_cast<const T*>(a.residual);
+    float* buf = dyn + grp.g * 64;
+    in.ring = reinterpret_cast<T*>(dyn + groups * 64) + (size_t)grp.g * STAGES * 2 * a.D;
+    in.D = a.D;
+    in.rank = grp.rank;
+    in.size = a.group;
     pdl_wait();
-    const size_t t = blockIdx.x, at = t * a.D;
-    const T* y = static_cast<const T*>(a.y) + at;
-    const T* res = static_cast<const T*>(a.residual) + at;
-    float v[ITER][V];
-    float ss = 0.f;
+    in.begin(t0, step, a.T);
+    const float inv = 1.f / a.D;
+    int parity = 0;
+    for (int t = t0; t < a.T; t += step) {
+        float v[ITER][V], ss[1] = {0.f};
+        in.wait();
 #pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * V;
-        if (c < a.D) {
-            load_f32<T, V>(y + c, v[i]);
+        for (int i = 0; i < ITER; ++i) {
+            if ((i * a.group + grp.rank) * V >= a.D) continue;
+            in.read(0, i, t, v[i]);
 #pragma unroll
-            for (int j = 0; j < V; ++j) ss = __fmaf_rn(v[i][j], v[i][j], ss);
+            for (int j = 0; j < V; ++j) ss[0] = __fmaf_rn(v[i][j], v[i][j], ss[0]);
         }
-    }
-    float ry = 1.f;
-    if (a.w_post) {
-        ry = rsqrtf(block_sum(ss, buf[0]) / a.D + a.eps);
-        if (a.rstd_post && threadIdx.x == 0) a.rstd_post[t] = ry;
-    }
-    const float gt = a.gate_mode == MOE_GATE_TOKEN ? __ldg(a.gate + t) : 1.f;
-    ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * V;
-        if (c >= a.D) continue;
-        float m[V];
+        float ry = 1.f;
         if (a.w_post) {
-            load_f32<float, V>(a.w_post + c, m);
-#pragma unroll
-            for (int j = 0; j < V; ++j) v[i][j] *= ry * m[j];
+            grp.sum(ss, buf, parity ^= 1);
+            ry = rsqrtf(__fmaf_rn(ss[0], inv, a.eps));
+            if (a.rstd_post && grp.rank == 0) a.rstd_post[t] = ry;
         }
-        if (a.gate_mode == MOE_GATE_CHANNEL) {
-            load_f32<float, V>(a.gate + c, m);
+        if (a.gate_mode == MOE_GATE_TOKEN) ry *= __ldg(a.gate + t);
+        ss[0] = 0.f;
 #pragma unroll
-            for (int j = 0; j < V; ++j) v[i][j] *= m[j];
-        } else if (a.gate_mode == MOE_GATE_TOKEN) {
+        for (int i = 0; i < ITER; ++i) {
+            const int c = (i * a.group + grp.rank) * V;
+            if (c >= a.D) continue;
+            float m[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) v[i][j] *= gt;
+            for (int j = 0; j < V; ++j) v[i][j] *= ry;
+            if (a.w_post) {
+                load_f32<float, V>(a.w_post + c, m);
+#pragma unroll
+                for (int j = 0; j < V; ++j) v[i][j] *= m[j];
+            }
+            if (a.gate_mode == MOE_GATE_CHANNEL) {
+                load_f32<float, V>(a.gate + c, m);
+#pragma unroll
+                for (int j = 0; j < V; ++j) v[i][j] *= m[j];
+            }
+            if (a.residual) {
+                in.read(1, i, t, m);
+#pragma unroll
+                for (int j = 0; j < V; ++j) v[i][j] = __fmaf_rn(a.alpha, m[j], v[i][j]);
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                v[i][j] = as_stored<T>(v[i][j]);
+                ss[0] = __fmaf_rn(v[i][j], v[i][j], ss[0]);
+            }
+            if (a.x_out) store_f32<T, V>(static_cast<T*>(a.x_out) + (size_t)t * a.D + c, v[i]);
         }
-        if (a.residual) {
-            load_f32<T, V>(res + c, m);
+        if (a.w_next) {
+            grp.sum(ss, buf, parity ^= 1);
+            const float rx = rsqrtf(__fmaf_rn(ss[0], inv, a.eps));
+            if (a.rstd_next && grp.rank == 0) a.rstd_next[t] = rx;
 #pragma unroll
-            for (int j = 0; j < V; ++j) v[i][j] = __fmaf_rn(a.alpha, m[j], v[i][j]);
+            for (int i = 0; i < ITER; ++i) {
+                const int c = (i * a.group + grp.rank) * V;
+                if (c >= a.D) continue;
+                float m[V];
+                load_f32<float, V>(a.w_next + c, m);
+#pragma unroll
+                for (int j = 0; j < V; ++j) m[j] *= v[i][j] * rx;
+                store_f32<T, V>(static_cast<T*>(a.normed) + (size_t)t * a.D + c, m);
+            }
         }
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            v[i][j] = as_stored<T>(v[i][j]);         // x_out as it is stored
-            ss = __fmaf_rn(v[i][j], v[i][j], ss);
-        }
-        if (a.x_out) store_f32<T, V>(static_cast<T*>(a.x_out) + at + c, v[i]);
-    }
-    if (!a.w_next) return;
-    const float rx = rsqrtf(block_sum(ss, buf[1]) / a.D + a.eps);
-    if (a.rstd_next && threadIdx.x == 0) a.rstd_next[t] = rx;
-#pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * V;
-        if (c >= a.D) continue;
-        float m[V];
-        load_f32<float, V>(a.w_next + c, m);
-#pragma unroll
-        for (int j = 0; j < V; ++j) m[j] *= v[i][j] * rx;
-        store_f32<T, V>(static_cast<T*>(a.normed) + at + c, m);
+        in.refill(t, step, a.T);
     }
 }
 
 struct NormGradArgs {
-    const void *dx_out, *dnormed, *x_out, *y;
+    const void *dx_out, *dnormed, *x_out, *y;   // dnormed, x_out: null without w_next; y: null if it is not read
     const float* gate;
     int gate_mode;
     float alpha;
     const float *w_post, *rstd_post, *w_next, *rstd_next;
-    int T, D;
+    int T, D, group;
     void *dy, *dresidual;
     float *dgate, *dw_post, *dw_next;
     float* part;                        // [gridDim.x][3][D]: dw_next, dw_post, dgate (channel)
 };
 
-// Blocks walk over the tokens t = blockIdx.x, + gridDim.x, ...; a thread owns
-// the same columns of all of them and keeps their weight gradients.
-template <typename T, int V, int ITER>
-__global__ void __launch_bounds__(1024) block_norm_backward_kernel(NormGradArgs a) {
-    __shared__ float buf[3][32];
-    pdl_wait();
-    float s_next[ITER][V], s_post[ITER][V], s_gate[ITER][V];
+// With q = yh w_post gate and G = b - r c1 xh, b = dx_out + r u, c1 = mean(xh u),
+// the second mean's sum is  sum(q G) = sum(q b) - r c1 sum(q xh):  all three sums
+// of a token are formed at once, with one barrier.  A token gate stays outside
+// of q: sum(q G) is then its gradient.
+//   SMEM: the sums over tokens are kept in shared memory, for rows too wide for
+//   the registers.
+template <typename T, int V, int ITER, int STAGES, int THREADS, bool SMEM>
+__global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 2 : 1) block_norm_backward_kernel(NormGradArgs a) {
+    extern __shared__ __align__(16) float dyn[];        // [2][3][32] per group, [3][D] sums, the groups' rings
+    const Group grp(a.group);
+    const int groups = blockDim.x / a.group, step = gridDim.x * groups, t0 = blockIdx.x * groups + grp.g;
+    float *buf = dyn + grp.g * 192, *sums = dyn + groups * 192;         // the sums: with SMEM or several groups
+    const bool joined = SMEM || groups > 1;
+    Rows<T, V, ITER, 4, STAGES> in;
+    in.src[0] = static_cast<const T*>(a.x_out);
+    in.src[1] = static_cast<const T*>(a.dnormed);
+    in.src[2] = static_cast<const T*>(a.dx_out);
+    in.src[3] = static_cast<const T*>(a.y);
+    in.ring = reinterpret_cast<T*>(sums + (joined ? 3 * a.D : 0)) + (size_t)grp.g * STAGES * 4 * a.D;
+    in.D = a.D;
+    in.rank = grp.rank;
+    in.size = a.group;
+    constexpr int N = SMEM ? 1 : ITER;
+    float s_next[N][V], s_post[N][V], s_gate[N][V];
 #pragma unroll
-    for (int i = 0; i < ITER; ++i)
+    for (int i = 0; i < N; ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j) s_next[i][j] = s_post[i][j] = s_gate[i][j] = 0.f;
-    for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-        const size_t at = (size_t)t * a.D;
+    if (SMEM) {
+        for (int i = threadIdx.x; i < 3 * a.D; i += blockDim.x) sums[i] = 0.f;
+        __syncthreads();
+    }
+    pdl_wait();
+    in.begin(t0, step, a.T);
+    const float inv = 1.f / a.D;
+    int parity = 0;
+    for (int t = t0; t < a.T; t += step, parity ^= 1) {
         const float rx = a.w_next ? __ldg(a.rstd_next + t) : 0.f;
         const float ry = a.w_post ? __ldg(a.rstd_post + t) : 1.f;
-        float g[ITER][V], xh[ITER][V];
-        float c1 = 0.f;
-#pragma unroll
-        for (int i = 0; i < ITER; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * V;
-#pragma unroll
-            for (int j = 0; j < V; ++j) g[i][j] = xh[i][j] = 0.f;
-            if (c >= a.D || !a.w_next) continue;
-            float w[V];
-            load_f32<T, V>(static_cast<const T*>(a.x_out) + at + c, xh[i]);
-            load_f32<T, V>(static_cast<const T*>(a.dnormed) + at + c, g[i]);
-            load_f32<float, V>(a.w_next + c, w);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                xh[i][j] *= rx;
-                s_next[i][j] = __fmaf_rn(g[i][j], xh[i][j], s_next[i][j]);
-                g[i][j] *= w[j];
-                c1 = __fmaf_rn(xh[i][j], g[i][j], c1);
-            }
-        }
-        if (a.w_next) c1 = block_sum(c1, buf[0]) / a.D;
         const float gt = a.gate_mode == MOE_GATE_TOKEN ? __ldg(a.gate + t) : 1.f;
-        float c2 = 0.f, dot = 0.f;
-        float yh[ITER][V];
+        float b[ITER][V], xh[ITER][V], yh[ITER][V];
+        float s[3] = {0.f, 0.f, 0.f};           // xh u, q b, q xh
+        in.wait();
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * V;
+            const int c = (i * a.group + grp.rank) * V;
             if (c >= a.D) continue;
             float m[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) g[i][j] = rx * (g[i][j] - xh[i][j] * c1);
-            if (a.dx_out) {
-                load_f32<T, V>(static_cast<const T*>(a.dx_out) + at + c, m);
+            for (int j = 0; j < V; ++j) b[i][j] = xh[i][j] = yh[i][j] = 0.f;
+            if (a.w_next) {
+                float w[V];
+                in.read(0, i, t, xh[i]);
+                in.read(1, i, t, m);
+                load_f32<float, V>(a.w_next + c, w);
 #pragma unroll
-                for (int j = 0; j < V; ++j) g[i][j] += m[j];
+                for (int j = 0; j < V; ++j) {
+                    xh[i][j] *= rx;
+                    if (!SMEM) s_next[i][j] = __fmaf_rn(m[j], xh[i][j], s_next[i][j]);
+                    w[j] *= m[j];
+                    s[0] = __fmaf_rn(xh[i][j], w[j], s[0]);
+                    b[i][j] = rx * w[j];
+                }
+                if (SMEM && a.dw_next) {
+                    load_f32<float, V>(sums + c, w);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) w[j] = __fmaf_rn(m[j], xh[i][j], w[j]);
+                    store_f32<float, V>(sums + c, w);
+                }
             }
+            if (a.dx_out) {
+                in.read(2, i, t, m);
+#pragma unroll
+                for (int j = 0; j < V; ++j) b[i][j] += m[j];
+            }
+            if (a.y) {
+                in.read(3, i, t, yh[i]);
+                float q[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) q[j] = yh[i][j] *= ry;
+                if (a.w_post) {
+                    load_f32<float, V>(a.w_post + c, m);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) q[j] *= m[j];
+                }
+                if (a.gate_mode == MOE_GATE_CHANNEL) {
+                    load_f32<float, V>(a.gate + c, m);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) q[j] *= m[j];
+                }
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    s[1] = __fmaf_rn(q[j], b[i][j], s[1]);
+                    s[2] = __fmaf_rn(q[j], xh[i][j], s[2]);
+                }
+            }
+        }
+        grp.sum(s, buf, parity);
+        in.refill(t, step, a.T);
+        const float rc1 = rx * s[0] * inv, sq = __fmaf_rn(-rc1, s[2], s[1]);
+        const float c2 = a.w_post ? gt * sq * inv : 0.f;
+        if (a.gate_mode == MOE_GATE_TOKEN && a.dgate && grp.rank == 0) a.dgate[t] = sq;
+#pragma unroll
+        for (int i = 0; i < ITER; ++i) {
+            const int c = (i * a.group + grp.rank) * V;
+            if (c >= a.D) continue;
+            const size_t at = (size_t)t * a.D + c;
+            float m[V], wp[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) b[i][j] = __fmaf_rn(-rc1, xh[i][j], b[i][j]);       // G
             if (a.dresidual) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) m[j] = a.alpha * g[i][j];
-                store_f32<T, V>(static_cast<T*>(a.dresidual) + at + c, m);
+                for (int j = 0; j < V; ++j) m[j] = a.alpha * b[i][j];
+                store_f32<T, V>(static_cast<T*>(a.dresidual) + at, m);
             }
-            float wp[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) wp[j] = 1.f, yh[i][j] = 0.f;
+            for (int j = 0; j < V; ++j) wp[j] = 1.f;
             if (a.w_post) load_f32<float, V>(a.w_post + c, wp);
-            if (a.w_post || a.dgate) {
-                load_f32<T, V>(static_cast<const T*>(a.y) + at + c, yh[i]);
+            if (a.gate_mode == MOE_GATE_CHANNEL) {
+                float sg[V];
+                if (SMEM && a.dgate) load_f32<float, V>(sums + 2 * a.D + c, sg);
+                load_f32<float, V>(a.gate + c, m);
 #pragma unroll
-                for (int j = 0; j < V; ++j) yh[i][j] *= ry;
+                for (int j = 0; j < V; ++j) {
+                    const float z = yh[i][j] * wp[j];
+                    if (SMEM) sg[j] = __fmaf_rn(b[i][j], z, sg[j]);
+                    else s_gate[i][j] = __fmaf_rn(b[i][j], z, s_gate[i][j]);
+                    b[i][j] *= m[j];                                                        // dz
+                }
+                if (SMEM && a.dgate) store_f32<float, V>(sums + 2 * a.D + c, sg);
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) b[i][j] *= gt;
+            }
+            if (SMEM && a.dw_post) {
+                load_f32<float, V>(sums + a.D + c, m);
+#pragma unroll
+                for (int j = 0; j < V; ++j) m[j] = __fmaf_rn(b[i][j], yh[i][j], m[j]);
+                store_f32<float, V>(sums + a.D + c, m);
             }
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float gz = g[i][j] * yh[i][j] * wp[j];
-                s_gate[i][j] += gz;
-                dot += gz;
-                m[j] = gt;
+                if (!SMEM) s_post[i][j] = __fmaf_rn(b[i][j], yh[i][j], s_post[i][j]);
+                m[j] = ry * __fmaf_rn(b[i][j], wp[j], -yh[i][j] * c2);
             }
-            if (a.gate_mode == MOE_GATE_CHANNEL) load_f32<float, V>(a.gate + c, m);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                g[i][j] *= m[j];                            // dz
-                s_post[i][j] = __fmaf_rn(g[i][j], yh[i][j], s_post[i][j]);
-                g[i][j] *= wp[j];
-                c2 = __fmaf_rn(yh[i][j], g[i][j], c2);
-            }
+            store_f32<T, V>(static_cast<T*>(a.dy) + at, m);
         }
-        if (a.gate_mode == MOE_GATE_TOKEN && a.dgate) {
-            dot = block_sum(dot, buf[2]);
-            if (threadIdx.x == 0) a.dgate[t] = dot;
-        }
-        if (a.w_post) c2 = block_sum(c2, buf[1]) / a.D;
-        else c2 = 0.f;
-#pragma unroll
-        for (int i = 0; i < ITER; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * V;
-            if (c >= a.D) continue;
-            float m[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j) m[j] = ry * (g[i][j] - yh[i][j] * c2);
-            store_f32<T, V>(static_cast<T*>(a.dy) + at + c, m);
-        }
-        __syncthreads();                                    // buf is used again by the next token
     }
+    // The block's sums: from the registers, or those of its groups added in order.
     float* part = a.part + (size_t)blockIdx.x * 3 * a.D;
+    for (int g = 0; !SMEM && g < groups; ++g) {
+        if (g == grp.g) {
 #pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-        const int c = (i * blockDim.x + threadIdx.x) * V;
-        if (c >= a.D) continue;
-        if (a.dw_next) store_f32<float, V>(part + c, s_next[i]);
-        if (a.dw_post) store_f32<float, V>(part + a.D + c, s_post[i]);
-        if (a.dgate && a.gate_mode == MOE_GATE_CHANNEL) store_f32<float, V>(part + 2 * a.D + c, s_gate[i]);
+            for (int i = 0; i < N; ++i) {
+                const int c = (i * a.group + grp.rank) * V;
+                if (c >= a.D) continue;
+                auto put = [&](int n, float (&v)[V]) {
+                    if (g > 0) {
+                        float w[V];
+                        load_f32<float, V>(sums + n * a.D + c, w);
+#pragma unroll
+                        for (int j = 0; j < V; ++j) v[j] += w[j];
+                    }
+                    store_f32<float, V>((g == groups - 1 ? part : sums) + n * a.D + c, v);
+                };
+                if (a.dw_next) put(0, s_next[i]);
+                if (a.dw_post) put(1, s_post[i]);
+                if (a.dgate && a.gate_mode == MOE_GATE_CHANNEL) put(2, s_gate[i]);
+            }
+        }
+        if (groups > 1) __syncthreads();
+    }
+    if (SMEM) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < 3 * a.D; i += blockDim.x) part[i] = sums[i];
     }
 }
 
-// Column sums of the blocks' partials, in block order.
+// Column sums of the blocks' partials: 32 columns per block, an eighth of the
+// partials per warp, the eighths added in order.
 __global__ void __launch_bounds__(256) block_norm_join_kernel(const float* __restrict__ part, int n, int D,
                                                               float* dw_next, float* dw_post, float* dgate) {
-    pdl_wait();
+    __shared__ float sums[8][32];
     float* out = blockIdx.y == 0 ? dw_next : blockIdx.y == 1 ? dw_post : dgate;
-    const int c = blockIdx.x * blockDim.x + threadIdx.x;
-    if (!out || c >= D) return;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    pdl_wait();
+    if (!out) return;
+    const int each = (n + 7) / 8, i1 = min(n, (w + 1) * each);
     float s = 0.f;
-    for (int i = 0; i < n; ++i) s += __ldg(part + ((size_t)i * 3 + blockIdx.y) * D + c);
-    out[c] = s;
+    if (c < D) {
+#pragma unroll 8
+        for (int i = w * each; i < i1; ++i) s += __ldg(part + ((size_t)i * 3 + blockIdx.y) * D + c);
+    }
+    sums[w][lane] = s;
+    __syncthreads();
+    if (w == 0 && c < D) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) s += sums[i][lane];
+        out[c] = s;
+    }
 }
 
-template <typename T, int V, int ITER>
-cudaError_t run_norm(const NormArgs& a, int T_, int threads, cudaStream_t s) {
-    return launch_pdl(block_norm_kernel<T, V, ITER>, dim3(T_), dim3(threads), 0, s, a);
+// Threads per token and tokens per block for rows of n packs per thread-iteration.
+struct NormShape {
+    int group, groups;
+    NormShape(int D, int per_thread) {
+        group = ((D + per_thread - 1) / per_thread + 31) / 32 * 32;
+        groups = group >= kNormThreads ? 1 : kNormThreads / group;
+        if (groups > kMaxGroups) groups = kMaxGroups;
+    }
+    int blocks(int T, int most) const {
+        const int n = (T + groups - 1) / groups;
+        return n < most ? n : most;
+    }
+};
+
+template <typename T, int V, int ITER, int STAGES, int THREADS>
+cudaError_t run_norm(NormArgs a, cudaStream_t s) {
+    auto kernel = block_norm_kernel<T, V, ITER, STAGES, THREADS>;
+    const NormShape n(a.D, V * ITER);
+    const size_t smem = (size_t)n.groups * (256 + STAGES * 2 * a.D * sizeof(T));
+    static std::atomic<uint64_t> set{0};
+    if (!once_per_device(set, [&] {
+            return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic) == cudaSuccess;
+        }))
+        return cudaErrorUnknown;
+    a.group = n.group;
+    const int per_sm = THREADS > 512 ? 1 : n.group * n.groups > kNormThreads ? 2 : 3;      // as their registers allow
+    return launch_pdl(kernel, dim3(n.blocks(a.T, device_sm_count() * per_sm)), dim3(n.group * n.groups), smem, s, a);
 }
-template <typename T, int V, int ITER>
-cudaError_t run_norm_backward(const NormGradArgs& a, int blocks, int threads, cudaStream_t s) {
-    return launch_pdl(block_norm_backward_kernel<T, V, ITER>, dim3(blocks), dim3(threads), 0, s, a);
+template <typename T, int V, int ITER, int STAGES, int THREADS, bool SMEM>
+cudaError_t run_norm_backward(NormGradArgs a, int* blocks, cudaStream_t s) {
+    auto kernel = block_norm_backward_kernel<T, V, ITER, STAGES, THREADS, SMEM>;
+    const NormShape n(a.D, V * ITER);
+    const size_t smem = (SMEM || n.groups > 1 ? (size_t)3 * a.D * 4 : 0) +
+                        (size_t)n.groups * (768 + STAGES * 4 * a.D * sizeof(T));
+    static std::atomic<uint64_t> set{0};
+    if (!once_per_device(set, [&] {
+            return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic) == cudaSuccess;
+        }))
+        return cudaErrorUnknown;
+    a.group = n.group;
+    const int sms = device_sm_count() < kNormParts / 2 ? device_sm_count() : kNormParts / 2;
+    *blocks = n.blocks(a.T, THREADS == kNormThreads ? 2 * sms : sms);
+    return launch_pdl(kernel, dim3(*blocks), dim3(n.group * n.groups), smem, s, a);
 }
 
-inline int warps_of(int n) { return (n + 31) / 32 * 32; }
-
-template <typename T, int V>
-cudaError_t pick_norm(const NormArgs& a, int T_, cudaStream_t s) {
-    const int n = (a.D + V - 1) / V;            // packs per token
-    if (n <= 1024) return run_norm<T, V, 1>(a, T_, warps_of(n), s);
-    if (n <= 2048) return run_norm<T, V, 2>(a, T_, 1024, s);
-    if (n <= 4096) return run_norm<T, V, 4>(a, T_, 1024, s);
-    return run_norm<T, V, 8>(a, T_, 1024, s);
+// Rows up to 4,096 elements keep their sums over tokens in registers (8 of each
+// per thread with 16-bit types, 4 with fp32); wider ones, and single elements
+// where the rows are not of 16-byte packs, as the limits of threads and
+// registers allow.
+template <typename T>
+cudaError_t pick_norm(const NormArgs& a, bool wide, cudaStream_t s) {
+    constexpr int V = 16 / sizeof(T);
+    if (!wide) {
+        if (a.D <= 2048) return run_norm<T, 1, 4, 0, 512>(a, s);
+        return run_norm<T, 1, 8, 0, 1024>(a, s);
+    }
+    if (a.D <= 512 * V) return run_norm<T, V, 1, 3, 512>(a, s);
+    if (a.D <= 1024 * V) return run_norm<T, V, 1, 3, 1024>(a, s);
+    return run_norm<T, V, sizeof(T) == 4 ? 2 : 1, 3, 1024>(a, s);
 }
-template <typename T, int V>
-cudaError_t pick_norm_backward(const NormGradArgs& a, int blocks, cudaStream_t s) {
-    const int n = (a.D + V - 1) / V;
-    if (n <= 1024) return run_norm_backward<T, V, 1>(a, blocks, warps_of(n), s);
-    if (n <= 2048) return run_norm_backward<T, V, 2>(a, blocks, 1024, s);
-    if (n <= 4096) return run_norm_backward<T, V, 4>(a, blocks, 1024, s);
-    return run_norm_backward<T, V, 8>(a, blocks, 1024, s);
+template <typename T>
+cudaError_t pick_norm_backward(const NormGradArgs& a, bool wide, int* blocks, cudaStream_t s) {
+    constexpr int V = 16 / sizeof(T);
+    if (!wide) {
+        if (a.D <= 4 * kNormThreads) return run_norm_backward<T, 1, 4, 0, kNormThreads, false>(a, blocks, s);
+        if (a.D <= 2048) return run_norm_backward<T, 1, 4, 0, 512, false>(a, blocks, s);
+        return run_norm_backward<T, 1, 8, 0, 1024, true>(a, blocks, s);
+    }
+    if (a.D <= kNormThreads * V) return run_norm_backward<T, V, 1, 3, kNormThreads, false>(a, blocks, s);
+    if (a.D <= 512 * V) return run_norm_backward<T, V, 1, 3, 512, false>(a, blocks, s);
+    if constexpr (sizeof(T) == 2) return run_norm_backward<T, V, 1, 2, 1024, true>(a, blocks, s);
+    else if (a.D <= 1024 * V) return run_norm_backward<T, V, 1, 2, 1024, false>(a, blocks, s);
+    else return run_norm_backward<T, V, 2, 0, 1024, true>(a, blocks, s);
 }
 
 moe_status norm_shapes(int T, int D) { return ops_shapes(T, 1, D); }
@@ -306,12 +520,8 @@ extern "C" moe_status moe_block_norm(const void* y, const void* residual, const 
     const bool wide = (D * es) % 16 == 0 && ops_aligned(y, 16) && ops_aligned(residual, 16) && ops_aligned(x_out, 16) &&
                       ops_aligned(normed, 16) && ops_aligned(w_post, 16) && ops_aligned(w_next, 16) &&
                       (gate_mode != MOE_GATE_CHANNEL || ops_aligned(gate, 16));
-    const NormArgs a{y, residual, gate, gate_mode, alpha, w_post, w_next, eps, D, x_out, normed, rstd_post, rstd_next};
-    cudaStream_t s = (cudaStream_t)stream;
-    return with_dtype(dtype, [&](auto e) {
-        using Tp = decltype(e);
-        return ops_status(wide ? pick_norm<Tp, 16 / sizeof(Tp)>(a, T, s) : pick_norm<Tp, 1>(a, T, s));
-    });
+    const NormArgs a{y, residual, gate, gate_mode, alpha, w_post, w_next, eps, T, D, 0, x_out, normed, rstd_post, rstd_next};
+    return with_dtype(dtype, [&](auto e) { return ops_status(pick_norm<decltype(e)>(a, wide, (cudaStream_t)stream)); });
 }
 
 extern "C" size_t moe_block_norm_backward_workspace_size(int T, int D) {
@@ -354,15 +564,12 @@ extern "C" moe_status moe_block_norm_backward(const void* dx_out, const void* dn
                       ops_aligned(x_out, 16) && ops_aligned(y, 16) && ops_aligned(dy, 16) &&
                       ops_aligned(dresidual, 16) && ops_aligned(w_post, 16) && ops_aligned(w_next, 16) &&
                       (gate_mode != MOE_GATE_CHANNEL || ops_aligned(gate, 16));
-    const int blocks = T < kNormParts ? T : kNormParts;
-    const NormGradArgs a{dx_out,    dnormed, x_out, y,  gate, gate_mode, alpha, w_post,  rstd_post, w_next,
-                         rstd_next, T,       D,     dy, dresidual, dgate, dw_post, dw_next, static_cast<float*>(ws)};
-    st = with_dtype(dtype, [&](auto e) {
-        using Tp = decltype(e);
-        return ops_status(wide ? pick_norm_backward<Tp, 16 / sizeof(Tp)>(a, blocks, s)
-                               : pick_norm_backward<Tp, 1>(a, blocks, s));
-    });
+    const NormGradArgs a{dx_out, w_next ? dnormed : nullptr, w_next ? x_out : nullptr, w_post || dgate ? y : nullptr,
+                         gate, gate_mode, alpha, w_post, rstd_post, w_next, rstd_next, T, D, 0, dy, dresidual, dgate,
+                         dw_post, dw_next, static_cast<float*>(ws)};
+    int blocks = 0;
+    st = with_dtype(dtype, [&](auto e) { return ops_status(pick_norm_backward<decltype(e)>(a, wide, &blocks, s)); });
     if (st != MOE_OK || (!dw_next && !dw_post && !dgate_cols)) return st;
-    return ops_status(launch_pdl(block_norm_join_kernel, dim3((D + 255) / 256, 3), dim3(256), 0, s,
+    return ops_status(launch_pdl(block_norm_join_kernel, dim3((D + 31) / 32, 3), dim3(256), 0, s,
                                  (const float*)ws, blocks, D, dw_next, dw_post, dgate_cols));
 }
