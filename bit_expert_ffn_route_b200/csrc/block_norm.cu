@@ -7,10 +7,13 @@
 // likewise: four rows in, two out.  HBM bounds both.
 //
 // Threads: a group of whole warps takes a token, each thread the same columns of
-// every token it takes, so that the sums over tokens stay in its registers;
-// short rows put several groups in a block.  Groups walk over the tokens and
-// fetch the rows of their next tokens with cp.async while they work: a thread
-// copies just what it will read itself, so no barrier guards the copies.
+// every token it takes, so that weights and the sums over tokens stay in its
+// registers; short rows put several groups in a block.  Groups walk over the
+// tokens and fetch the rows of their next tokens with cp.async while they work.
+// Rows of whole 16-byte packs: a thread copies just what it will read itself, so
+// no barrier guards the copies.  Other rows start anywhere: the 16-byte blocks
+// that cover the row are copied (elements where such a block reaches over the
+// buffer's ends), and read back an element at a time behind a barrier.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -21,10 +24,10 @@
 namespace moe {
 namespace {
 
-constexpr int kNormParts = 296;        // most blocks of the backward pass: two per SM, a partial of each weight gradient from every one
+constexpr int kNormParts = 296;        // most blocks of the backward pass: two per SM, a partial of each sum over tokens from every one
 constexpr int kNormThreads = 384;      // threads that the groups of a block fill, about
-constexpr int kMaxDynamic = 227 * 1024;
 constexpr int kMaxGroups = 12;         // named barriers 1..12
+constexpr int kMaxDynamic = 227 * 1024;
 
 template <int N>
 MOE_DEVINL void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -33,71 +36,184 @@ MOE_DEVINL void cp_async16(void* to, const void* from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
 }
 
-// A group's threads: rank in the group, its warps, and sums over them.
+// Elementwise on N (even) fp32 values, two per instruction; each product and
+// multiply-add rounds as the scalar instruction does.
+#define MOE_F32X2(OP, D0, D1, A0, A1, B0, B1)                                                                     \
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t" OP                             \
+        " a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"                                                                  \
+        : "=f"(D0), "=f"(D1)                                                                                      \
+        : "f"(A0), "f"(A1), "f"(B0), "f"(B1))
+template <int N>
+MOE_DEVINL void mul(float (&d)[N], const float (&a)[N], const float (&b)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) MOE_F32X2("mul.rn.f32x2", d[i], d[i + 1], a[i], a[i + 1], b[i], b[i + 1]);
+}
+template <int N>
+MOE_DEVINL void mul(float (&d)[N], const float (&a)[N], float b) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) MOE_F32X2("mul.rn.f32x2", d[i], d[i + 1], a[i], a[i + 1], b, b);
+}
+MOE_DEVINL void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1, float c0, float c1) {
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+// d = a b + c
+template <int N>
+MOE_DEVINL void fma(float (&d)[N], const float (&a)[N], const float (&b)[N], const float (&c)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) fma2(d[i], d[i + 1], a[i], a[i + 1], b[i], b[i + 1], c[i], c[i + 1]);
+}
+template <int N>
+MOE_DEVINL void fma(float (&d)[N], const float (&a)[N], float b, const float (&c)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) fma2(d[i], d[i + 1], a[i], a[i + 1], b, b, c[i], c[i + 1]);
+}
+// sum of a b over the N values
+template <int N>
+MOE_DEVINL float dot(const float (&a)[N], const float (&b)[N]) {
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; i += 2) fma2(s0, s1, a[i], a[i + 1], b[i], b[i + 1], s0, s1);
+    return s0 + s1;
+}
+
+// A group's threads, and sums over them: the same bits in every thread, formed
+// in a fixed order (lanes, then warps).  buf: [2][4][32] floats of this group;
+// parity alternates from call to call, so one barrier per call is enough.
 struct Group {
     int g, rank, size;                          // group in the block, thread in the group, threads per group
-    MOE_DEVINL explicit Group(int threads) : g(threadIdx.x / threads), rank(threadIdx.x % threads), size(threads) {}
-    // N sums over the group, the same bits in every thread: lanes, then warps, in
-    // a fixed order.  buf: [2][N][32] floats of this group; parity alternates
-    // from call to call, so one barrier per call is enough.
-    template <int N>
-    MOE_DEVINL void sum(float (&v)[N], float* buf, int parity) const {
+    float* buf;
+    int parity = 0;
+    MOE_DEVINL void sync() const {
+        if (size == 32) __syncwarp();
+        else asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(size) : "memory");
+    }
+    MOE_DEVINL float sum(float v) {
         const int lane = threadIdx.x & 31;
+        v = warp_sum(v);
+        if (size == 32) return v;
+        float* b = buf + (parity ^= 128);
+        if (lane == 0) b[rank / 32] = v;
+        sync();
+        return warp_sum(lane < size / 32 ? b[lane] : 0.f);
+    }
+    // Three sums at once: lanes hand halves over, so that after two steps a lane
+    // is left with one of the three (or zero).
+    MOE_DEVINL void sum3(float& v0, float& v1, float& v2) {
+        const int lane = threadIdx.x & 31;
+        const bool hi = lane & 16, odd = lane & 8;
+        const float k0 = (hi ? v2 : v0) + __shfl_xor_sync(0xffffffffu, hi ? v0 : v2, 16);
+        const float k1 = (hi ? 0.f : v1) + __shfl_xor_sync(0xffffffffu, hi ? v1 : 0.f, 16);
+        float v = (odd ? k1 : k0) + __shfl_xor_sync(0xffffffffu, odd ? k0 : k1, 8);
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-        if (size == 32) return;
-        float* b = buf + parity * N * 32;
-        if (lane == 0) {
+        for (int o = 4; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (size > 32) {                        // lane 8 i holds sum 0, 1, 2, -, of this warp
+            float* b = buf + (parity ^= 128);
+            if (lane % 8 == 0) b[rank / 32 * 4 + lane / 8] = v;
+            sync();
+            v = 0.f;
+            for (int w = lane % 8; w < size / 32; w += 8) v += b[w * 4 + lane / 8];
 #pragma unroll
-            for (int i = 0; i < N; ++i) b[i * 32 + rank / 32] = v[i];
+            for (int o = 4; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         }
-        asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(size) : "memory");
+        v0 = __shfl_sync(0xffffffffu, v, 0);
+        v1 = __shfl_sync(0xffffffffu, v, 8);
+        v2 = __shfl_sync(0xffffffffu, v, 16);
+    }
+};
+constexpr int kSumFloats = 256;
+
+// Thread `rank` of a group of `size` owns N elements of a row: packs of V, at
+// (i size + rank) V (V = 1: single elements of rows that start anywhere).
+template <typename T, int N, bool WIDE>
+struct Cols {
+    static constexpr int V = WIDE ? (N < 16 / (int)sizeof(T) ? N : 16 / (int)sizeof(T)) : 1, ITER = N / V;
+    int rank, size, D;
+    MOE_DEVINL int at(int i) const { return (i * size + rank) * V; }
+    // Elements outside the row are zero.
+    template <typename S>
+    MOE_DEVINL void load(const S* p, float (&v)[N]) const {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = warp_sum(lane < size / 32 ? b[i * 32 + lane] : 0.f);
+        for (int i = 0; i < ITER; ++i) {
+            float w[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) w[j] = 0.f;
+            if (at(i) < D) load_f32<S, V>(p + at(i), w);
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[i * V + j] = w[j];
+        }
+    }
+    template <typename S>
+    MOE_DEVINL void store(S* p, const float (&v)[N]) const {
+#pragma unroll
+        for (int i = 0; i < ITER; ++i) {
+            float w[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) w[j] = v[i * V + j];
+            if (at(i) < D) store_f32<S, V>(p + at(i), w);
+        }
     }
 };
 
-// The rows of a group's coming tokens: STAGES tokens ahead in shared memory
-// (16-byte packs), or read when they are wanted (STAGES 0).
-template <typename T, int V, int ITER, int ROWS, int STAGES>
-struct Rows {
+// The rows of a group's coming tokens, STAGES tokens ahead in shared memory.
+template <typename T, int N, int ROWS, int STAGES, bool WIDE>
+struct Ring {
     const T* src[ROWS];                         // null: no such row
-    T* ring;                                    // [STAGES][ROWS][D] of this group
-    int D, rank, size, stage = 0;
-    MOE_DEVINL void fetch(int t, int T_, int to) {
-        if constexpr (STAGES > 0) {
-            if (t < T_) {
+    char* ring;                                 // [STAGES][ROWS][pitch] of this group
+    int pitch, T_, stage = 0;
+    Cols<T, N, WIDE> col;
+    MOE_DEVINL char* slot(int st, int r) const { return ring + (st * ROWS + r) * pitch; }
+    // bytes from the row's place in its slot to its first element
+    MOE_DEVINL int lead(int r, int t) const {
+        return WIDE ? 0 : (int)((uintptr_t)(src[r] + (size_t)t * col.D) & 15);
+    }
+    MOE_DEVINL void fetch(int t, int st) {
+        if (t < T_) {
 #pragma unroll
-                for (int r = 0; r < ROWS; ++r)
+            for (int r = 0; r < ROWS; ++r) {
+                if (!src[r]) continue;
+                const T* row = src[r] + (size_t)t * col.D;
+                char* to = slot(st, r);
+                if constexpr (WIDE) {
 #pragma unroll
-                    for (int i = 0; i < ITER; ++i) {
-                        const int c = (i * size + rank) * V;
-                        if (src[r] && c < D) cp_async16(ring + (size_t)(to * ROWS + r) * D + c, src[r] + (size_t)t * D + c);
+                    for (int i = 0; i < Cols<T, N, WIDE>::ITER; ++i)
+                        if (col.at(i) < col.D) cp_async16(to + col.at(i) * sizeof(T), row + col.at(i));
+                } else {
+                    const char* lo = reinterpret_cast<const char*>(src[r]);             // the buffer
+                    const char* hi = lo + (size_t)T_ * col.D * sizeof(T);
+                    const char* from = reinterpret_cast<const char*>(row) - lead(r, t);
+                    const int bytes = lead(r, t) + col.D * (int)sizeof(T);
+                    for (int j = col.rank * 16; j < bytes; j += col.size * 16) {
+                        if (from + j >= lo && from + j + 16 <= hi) {
+                            cp_async16(to + j, from + j);
+                        } else {
+                            for (int q = j; q < j + 16; q += sizeof(T))
+                                if (from + q >= lo && from + q < hi)
+                                    *reinterpret_cast<T*>(to + q) = *reinterpret_cast<const T*>(from + q);
+                        }
                     }
+                }
             }
-            cp_async_commit();
         }
+        cp_async_commit();
     }
-    MOE_DEVINL void begin(int t0, int step, int T_) {
-        if constexpr (STAGES > 0) {
+    MOE_DEVINL void begin(int t0, int step) {
 #pragma unroll
-            for (int i = 0; i < STAGES; ++i) fetch(t0 + i * step, T_, i);
-        }
+        for (int i = 0; i < STAGES; ++i) fetch(t0 + i * step, i);
     }
-    MOE_DEVINL void wait() const {
-        if constexpr (STAGES > 0) cp_async_wait<STAGES - 1>();
+    MOE_DEVINL void wait(const Group& grp) const {
+        cp_async_wait<STAGES - 1>();
+        if (!WIDE) grp.sync();
     }
-    MOE_DEVINL void read(int r, int i, int t, float (&v)[V]) const {
-        const int c = (i * size + rank) * V;
-        if constexpr (STAGES > 0) load_f32<T, V>(ring + (size_t)(stage * ROWS + r) * D + c, v);
-        else load_f32<T, V>(src[r] + (size_t)t * D + c, v);
+    MOE_DEVINL void read(int r, int t, float (&v)[N]) const {
+        col.load(reinterpret_cast<const T*>(slot(stage, r) + lead(r, t)), v);
     }
-    // The token's rows have been read and used: fetch those of a later one in their place.
-    MOE_DEVINL void refill(int t, int step, int T_) {
-        if constexpr (STAGES > 0) {
-            fetch(t + STAGES * step, T_, stage);
-            stage = stage + 1 == STAGES ? 0 : stage + 1;
-        }
+    // The group has read token t's rows: fetch those of a later token in their place.
+    MOE_DEVINL void refill(int t, int step) {
+        fetch(t + STAGES * step, stage);
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
 };
 
@@ -108,91 +224,66 @@ struct NormArgs {
     float alpha;
     const float *w_post, *w_next;
     float eps;
-    int T, D, group;                            // group: threads per token
+    int T, D, group, pitch;                     // group: threads per token; pitch: bytes of a row's slot
     void *x_out, *normed;
     float *rstd_post, *rstd_next;
 };
 
-template <typename T, int V, int ITER, int STAGES, int THREADS>
+template <typename T, int N, int STAGES, int THREADS, bool WIDE>
 __global__ void __launch_bounds__(THREADS) block_norm_kernel(NormArgs a) {
-    extern __shared__ __align__(16) float dyn[];        // of every group: [2][32] for its sums; its ring
-    const Group grp(a.group);
-    const int groups = blockDim.x / a.group, step = gridDim.x * groups, t0 = blockIdx.x * groups + grp.g;
-    Rows<T, V, ITER, 2, STAGES> in;
-    in.src[0] = static_cast<const T*>(a.y);
-    in.src[1] = static_cast<const T*>(a.residual);
-    float* buf = dyn + grp.g * 64;
-    in.ring = reinterpret_cast<T*>(dyn + groups * 64) + (size_t)grp.g * STAGES * 2 * a.D;
-    in.D = a.D;
-    in.rank = grp.rank;
-    in.size = a.group;
+    extern __shared__ __align__(16) float dyn[];        // sums, then rings, of every group
+    const int groups = blockDim.x / a.group, g = threadIdx.x / a.group, rank = threadIdx.x % a.group;
+    const int step = gridDim.x * groups, t0 = blockIdx.x * groups + g;
+    Group grp{g, rank, a.group, dyn + g * kSumFloats};
+    const Cols<T, N, WIDE> col{rank, a.group, a.D};
+    Ring<T, N, 2, STAGES, WIDE> in{{static_cast<const T*>(a.y), static_cast<const T*>(a.residual)},
+                                   reinterpret_cast<char*>(dyn + groups * kSumFloats) + g * STAGES * 2 * a.pitch,
+                                   a.pitch, a.T, 0, col};
     pdl_wait();
-    in.begin(t0, step, a.T);
+    in.begin(t0, step);
+    // the columns' factors: w_post times a channel gate, and w_next
+    float gw[N], wn[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) gw[j] = wn[j] = 1.f;
+    if (a.w_post) col.load(a.w_post, gw);
+    if (a.gate_mode == MOE_GATE_CHANNEL) {
+        col.load(a.gate, wn);
+        mul(gw, gw, wn);
+    }
+    if (a.w_next) col.load(a.w_next, wn);
     const float inv = 1.f / a.D;
-    int parity = 0;
     for (int t = t0; t < a.T; t += step) {
-        float v[ITER][V], ss[1] = {0.f};
-        in.wait();
+        float v[N], r[N];
+        float f = a.gate_mode == MOE_GATE_TOKEN ? __ldg(a.gate + t) : 1.f;
+        in.wait(grp);
+        in.read(0, t, v);
+        if (a.residual) {
+            in.read(1, t, r);
+            mul(r, r, a.alpha);
+        } else {
 #pragma unroll
-        for (int i = 0; i < ITER; ++i) {
-            if ((i * a.group + grp.rank) * V >= a.D) continue;
-            in.read(0, i, t, v[i]);
-#pragma unroll
-            for (int j = 0; j < V; ++j) ss[0] = __fmaf_rn(v[i][j], v[i][j], ss[0]);
+            for (int j = 0; j < N; ++j) r[j] = 0.f;
         }
-        float ry = 1.f;
         if (a.w_post) {
-            grp.sum(ss, buf, parity ^= 1);
-            ry = rsqrtf(__fmaf_rn(ss[0], inv, a.eps));
-            if (a.rstd_post && grp.rank == 0) a.rstd_post[t] = ry;
+            const float ry = rsqrtf(__fmaf_rn(grp.sum(dot(v, v)), inv, a.eps));
+            if (a.rstd_post && rank == 0) a.rstd_post[t] = ry;
+            f *= ry;
         }
-        if (a.gate_mode == MOE_GATE_TOKEN) ry *= __ldg(a.gate + t);
-        ss[0] = 0.f;
+        mul(v, v, gw);
+        fma(v, v, f, r);
 #pragma unroll
-        for (int i = 0; i < ITER; ++i) {
-            const int c = (i * a.group + grp.rank) * V;
-            if (c >= a.D) continue;
-            float m[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j) v[i][j] *= ry;
-            if (a.w_post) {
-                load_f32<float, V>(a.w_post + c, m);
-#pragma unroll
-                for (int j = 0; j < V; ++j) v[i][j] *= m[j];
-            }
-            if (a.gate_mode == MOE_GATE_CHANNEL) {
-                load_f32<float, V>(a.gate + c, m);
-#pragma unroll
-                for (int j = 0; j < V; ++j) v[i][j] *= m[j];
-            }
-            if (a.residual) {
-                in.read(1, i, t, m);
-#pragma unroll
-                for (int j = 0; j < V; ++j) v[i][j] = __fmaf_rn(a.alpha, m[j], v[i][j]);
-            }
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                v[i][j] = as_stored<T>(v[i][j]);
-                ss[0] = __fmaf_rn(v[i][j], v[i][j], ss[0]);
-            }
-            if (a.x_out) store_f32<T, V>(static_cast<T*>(a.x_out) + (size_t)t * a.D + c, v[i]);
-        }
+        for (int j = 0; j < N; ++j) v[j] = as_stored<T>(v[j]);
+        if (a.x_out) col.store(static_cast<T*>(a.x_out) + (size_t)t * a.D, v);
         if (a.w_next) {
-            grp.sum(ss, buf, parity ^= 1);
-            const float rx = rsqrtf(__fmaf_rn(ss[0], inv, a.eps));
-            if (a.rstd_next && grp.rank == 0) a.rstd_next[t] = rx;
-#pragma unroll
-            for (int i = 0; i < ITER; ++i) {
-                const int c = (i * a.group + grp.rank) * V;
-                if (c >= a.D) continue;
-                float m[V];
-                load_f32<float, V>(a.w_next + c, m);
-#pragma unroll
-                for (int j = 0; j < V; ++j) m[j] *= v[i][j] * rx;
-                store_f32<T, V>(static_cast<T*>(a.normed) + (size_t)t * a.D + c, m);
-            }
+            const float rx = rsqrtf(__fmaf_rn(grp.sum(dot(v, v)), inv, a.eps));
+            if (a.rstd_next && rank == 0) a.rstd_next[t] = rx;
+            mul(v, v, wn);
+            mul(v, v, rx);
+            col.store(static_cast<T*>(a.normed) + (size_t)t * a.D, v);
+        } else if (!WIDE) {
+            grp.sync();                         // all of the group have read the token
         }
-        in.refill(t, step, a.T);
+        in.refill(t, step);
     }
 }
 
@@ -202,221 +293,172 @@ struct NormGradArgs {
     int gate_mode;
     float alpha;
     const float *w_post, *rstd_post, *w_next, *rstd_next;
-    int T, D, group;
+    int T, D, group, pitch;
     void *dy, *dresidual;
-    float *dgate, *dw_post, *dw_next;
-    float* part;                        // [gridDim.x][3][D]: dw_next, dw_post, dgate (channel)
+    float* dgate;                               // of a token gate
+    bool want_next, want_post;                  // the sums over tokens that part gets
+    float* part;                                // [gridDim.x][2][D]: of dnormed xh, of G yh (times a token gate)
 };
 
 // With q = yh w_post gate and G = b - r c1 xh, b = dx_out + r u, c1 = mean(xh u),
 // the second mean's sum is  sum(q G) = sum(q b) - r c1 sum(q xh):  all three sums
 // of a token are formed at once, with one barrier.  A token gate stays outside
-// of q: sum(q G) is then its gradient.
+// of q: sum(q G) is then its gradient.  A channel gate and w_post are the same
+// for all tokens, so both their gradients come from the sums of G yh.
 //   SMEM: the sums over tokens are kept in shared memory, for rows too wide for
 //   the registers.
-template <typename T, int V, int ITER, int STAGES, int THREADS, bool SMEM>
+template <typename T, int N, int STAGES, int THREADS, bool SMEM, bool WIDE>
 __global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 2 : 1) block_norm_backward_kernel(NormGradArgs a) {
-    extern __shared__ __align__(16) float dyn[];        // [2][3][32] per group, [3][D] sums, the groups' rings
-    const Group grp(a.group);
-    const int groups = blockDim.x / a.group, step = gridDim.x * groups, t0 = blockIdx.x * groups + grp.g;
-    float *buf = dyn + grp.g * 192, *sums = dyn + groups * 192;         // the sums: with SMEM or several groups
-    const bool joined = SMEM || groups > 1;
-    Rows<T, V, ITER, 4, STAGES> in;
-    in.src[0] = static_cast<const T*>(a.x_out);
-    in.src[1] = static_cast<const T*>(a.dnormed);
-    in.src[2] = static_cast<const T*>(a.dx_out);
-    in.src[3] = static_cast<const T*>(a.y);
-    in.ring = reinterpret_cast<T*>(sums + (joined ? 3 * a.D : 0)) + (size_t)grp.g * STAGES * 4 * a.D;
-    in.D = a.D;
-    in.rank = grp.rank;
-    in.size = a.group;
-    constexpr int N = SMEM ? 1 : ITER;
-    float s_next[N][V], s_post[N][V], s_gate[N][V];
+    extern __shared__ __align__(16) float dyn[];        // the groups' sums, [2][D] sums over tokens, the groups' rings
+    const int groups = blockDim.x / a.group, g = threadIdx.x / a.group, rank = threadIdx.x % a.group;
+    const int step = gridDim.x * groups, t0 = blockIdx.x * groups + g;
+    Group grp{g, rank, a.group, dyn + g * kSumFloats};
+    const Cols<T, N, WIDE> col{rank, a.group, a.D};
+    float* sums = dyn + groups * kSumFloats;            // with SMEM or several groups
+    const int sums_floats = SMEM || groups > 1 ? (2 * a.D + 3) / 4 * 4 : 0;
+    Ring<T, N, 4, STAGES, WIDE> in{{static_cast<const T*>(a.x_out), static_cast<const T*>(a.dnormed),
+                                    static_cast<const T*>(a.dx_out), static_cast<const T*>(a.y)},
+                                   reinterpret_cast<char*>(sums + sums_floats) + g * STAGES * 4 * a.pitch,
+                                   a.pitch, a.T, 0, col};
+    constexpr int M = SMEM ? 2 : N;
+    float s_next[M], s_gy[M];
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) s_next[i][j] = s_post[i][j] = s_gate[i][j] = 0.f;
+    for (int j = 0; j < M; ++j) s_next[j] = s_gy[j] = 0.f;
     if (SMEM) {
-        for (int i = threadIdx.x; i < 3 * a.D; i += blockDim.x) sums[i] = 0.f;
+        for (int i = threadIdx.x; i < 2 * a.D; i += blockDim.x) sums[i] = 0.f;
         __syncthreads();
     }
     pdl_wait();
-    in.begin(t0, step, a.T);
+    in.begin(t0, step);
+    float gw[N], wn[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) gw[j] = wn[j] = 1.f;
+    if (a.w_post) col.load(a.w_post, gw);
+    if (a.gate_mode == MOE_GATE_CHANNEL) {
+        col.load(a.gate, wn);
+        mul(gw, gw, wn);
+    }
+    if (a.w_next) col.load(a.w_next, wn);
     const float inv = 1.f / a.D;
-    int parity = 0;
-    for (int t = t0; t < a.T; t += step, parity ^= 1) {
+    for (int t = t0; t < a.T; t += step) {
         const float rx = a.w_next ? __ldg(a.rstd_next + t) : 0.f;
         const float ry = a.w_post ? __ldg(a.rstd_post + t) : 1.f;
         const float gt = a.gate_mode == MOE_GATE_TOKEN ? __ldg(a.gate + t) : 1.f;
-        float b[ITER][V], xh[ITER][V], yh[ITER][V];
-        float s[3] = {0.f, 0.f, 0.f};           // xh u, q b, q xh
-        in.wait();
+        float b[N], xh[N], yh[N], m[N];
+        float s0 = 0.f, s1 = 0.f, s2 = 0.f;     // sums of xh u, q b, q xh
+        in.wait(grp);
 #pragma unroll
-        for (int i = 0; i < ITER; ++i) {
-            const int c = (i * a.group + grp.rank) * V;
-            if (c >= a.D) continue;
-            float m[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j) b[i][j] = xh[i][j] = yh[i][j] = 0.f;
-            if (a.w_next) {
-                float w[V];
-                in.read(0, i, t, xh[i]);
-                in.read(1, i, t, m);
-                load_f32<float, V>(a.w_next + c, w);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    xh[i][j] *= rx;
-                    if (!SMEM) s_next[i][j] = __fmaf_rn(m[j], xh[i][j], s_next[i][j]);
-                    w[j] *= m[j];
-                    s[0] = __fmaf_rn(xh[i][j], w[j], s[0]);
-                    b[i][j] = rx * w[j];
-                }
-                if (SMEM && a.dw_next) {
-                    load_f32<float, V>(sums + c, w);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) w[j] = __fmaf_rn(m[j], xh[i][j], w[j]);
-                    store_f32<float, V>(sums + c, w);
-                }
+        for (int j = 0; j < N; ++j) b[j] = xh[j] = yh[j] = 0.f;
+        if (a.dx_out) in.read(2, t, b);
+        if (a.w_next) {
+            in.read(0, t, xh);
+            in.read(1, t, m);
+            mul(xh, xh, rx);
+            if constexpr (!SMEM) {
+                fma(s_next, m, xh, s_next);
+            } else if (a.want_next) {
+                float acc[N];
+                col.load(sums, acc);
+                fma(acc, m, xh, acc);
+                col.store(sums, acc);
             }
-            if (a.dx_out) {
-                in.read(2, i, t, m);
-#pragma unroll
-                for (int j = 0; j < V; ++j) b[i][j] += m[j];
-            }
-            if (a.y) {
-                in.read(3, i, t, yh[i]);
-                float q[V];
-#pragma unroll
-                for (int j = 0; j < V; ++j) q[j] = yh[i][j] *= ry;
-                if (a.w_post) {
-                    load_f32<float, V>(a.w_post + c, m);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) q[j] *= m[j];
-                }
-                if (a.gate_mode == MOE_GATE_CHANNEL) {
-                    load_f32<float, V>(a.gate + c, m);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) q[j] *= m[j];
-                }
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    s[1] = __fmaf_rn(q[j], b[i][j], s[1]);
-                    s[2] = __fmaf_rn(q[j], xh[i][j], s[2]);
-                }
-            }
+            mul(m, m, wn);                      // u
+            s0 = dot(xh, m);
+            fma(b, m, rx, b);
         }
-        grp.sum(s, buf, parity);
-        in.refill(t, step, a.T);
-        const float rc1 = rx * s[0] * inv, sq = __fmaf_rn(-rc1, s[2], s[1]);
+        if (a.y) {
+            in.read(3, t, yh);
+            mul(yh, yh, ry);
+            mul(m, yh, gw);                     // q
+            s1 = dot(m, b);
+            s2 = dot(m, xh);
+        }
+        grp.sum3(s0, s1, s2);
+        in.refill(t, step);
+        const float rc1 = rx * s0 * inv, sq = __fmaf_rn(-rc1, s2, s1);
         const float c2 = a.w_post ? gt * sq * inv : 0.f;
-        if (a.gate_mode == MOE_GATE_TOKEN && a.dgate && grp.rank == 0) a.dgate[t] = sq;
-#pragma unroll
-        for (int i = 0; i < ITER; ++i) {
-            const int c = (i * a.group + grp.rank) * V;
-            if (c >= a.D) continue;
-            const size_t at = (size_t)t * a.D + c;
-            float m[V], wp[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j) b[i][j] = __fmaf_rn(-rc1, xh[i][j], b[i][j]);       // G
-            if (a.dresidual) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) m[j] = a.alpha * b[i][j];
-                store_f32<T, V>(static_cast<T*>(a.dresidual) + at, m);
-            }
-#pragma unroll
-            for (int j = 0; j < V; ++j) wp[j] = 1.f;
-            if (a.w_post) load_f32<float, V>(a.w_post + c, wp);
-            if (a.gate_mode == MOE_GATE_CHANNEL) {
-                float sg[V];
-                if (SMEM && a.dgate) load_f32<float, V>(sums + 2 * a.D + c, sg);
-                load_f32<float, V>(a.gate + c, m);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float z = yh[i][j] * wp[j];
-                    if (SMEM) sg[j] = __fmaf_rn(b[i][j], z, sg[j]);
-                    else s_gate[i][j] = __fmaf_rn(b[i][j], z, s_gate[i][j]);
-                    b[i][j] *= m[j];                                                        // dz
-                }
-                if (SMEM && a.dgate) store_f32<float, V>(sums + 2 * a.D + c, sg);
-            } else {
-#pragma unroll
-                for (int j = 0; j < V; ++j) b[i][j] *= gt;
-            }
-            if (SMEM && a.dw_post) {
-                load_f32<float, V>(sums + a.D + c, m);
-#pragma unroll
-                for (int j = 0; j < V; ++j) m[j] = __fmaf_rn(b[i][j], yh[i][j], m[j]);
-                store_f32<float, V>(sums + a.D + c, m);
-            }
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                if (!SMEM) s_post[i][j] = __fmaf_rn(b[i][j], yh[i][j], s_post[i][j]);
-                m[j] = ry * __fmaf_rn(b[i][j], wp[j], -yh[i][j] * c2);
-            }
-            store_f32<T, V>(static_cast<T*>(a.dy) + at, m);
+        if (a.dgate && rank == 0) a.dgate[t] = sq;
+        fma(b, xh, -rc1, b);                    // G
+        if (a.dresidual) {
+            mul(m, b, a.alpha);
+            col.store(static_cast<T*>(a.dresidual) + (size_t)t * a.D, m);
         }
+        mul(b, b, gt);
+        if constexpr (!SMEM) {
+            fma(s_gy, b, yh, s_gy);
+        } else if (a.want_post) {
+            col.load(sums + a.D, m);
+            fma(m, b, yh, m);
+            col.store(sums + a.D, m);
+        }
+        mul(b, b, gw);
+        if (a.w_post) fma(b, yh, -c2, b);
+        mul(b, b, ry);
+        col.store(static_cast<T*>(a.dy) + (size_t)t * a.D, b);
     }
     // The block's sums: from the registers, or those of its groups added in order.
-    float* part = a.part + (size_t)blockIdx.x * 3 * a.D;
-    for (int g = 0; !SMEM && g < groups; ++g) {
-        if (g == grp.g) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int c = (i * a.group + grp.rank) * V;
-                if (c >= a.D) continue;
-                auto put = [&](int n, float (&v)[V]) {
-                    if (g > 0) {
-                        float w[V];
-                        load_f32<float, V>(sums + n * a.D + c, w);
-#pragma unroll
-                        for (int j = 0; j < V; ++j) v[j] += w[j];
-                    }
-                    store_f32<float, V>((g == groups - 1 ? part : sums) + n * a.D + c, v);
-                };
-                if (a.dw_next) put(0, s_next[i]);
-                if (a.dw_post) put(1, s_post[i]);
-                if (a.dgate && a.gate_mode == MOE_GATE_CHANNEL) put(2, s_gate[i]);
-            }
-        }
-        if (groups > 1) __syncthreads();
-    }
-    if (SMEM) {
+    float* part = a.part + (size_t)blockIdx.x * 2 * a.D;
+    if constexpr (SMEM) {
         __syncthreads();
-        for (int i = threadIdx.x; i < 3 * a.D; i += blockDim.x) part[i] = sums[i];
+        for (int i = threadIdx.x; i < 2 * a.D; i += blockDim.x) part[i] = sums[i];
+    } else {
+        for (int i = 0; i < groups; ++i) {
+            if (i == g) {
+                float w[N];
+                float* to = i == groups - 1 ? part : sums;
+                if (i > 0) {
+                    col.load(sums, w);
+#pragma unroll
+                    for (int j = 0; j < N; ++j) s_next[j] += w[j];
+                    col.load(sums + a.D, w);
+#pragma unroll
+                    for (int j = 0; j < N; ++j) s_gy[j] += w[j];
+                }
+                if (a.want_next) col.store(to, s_next);
+                if (a.want_post) col.store(to + a.D, s_gy);
+            }
+            if (groups > 1) __syncthreads();
+        }
     }
 }
 
 // Column sums of the blocks' partials: 32 columns per block, an eighth of the
 // partials per warp, the eighths added in order.
 __global__ void __launch_bounds__(256) block_norm_join_kernel(const float* __restrict__ part, int n, int D,
-                                                              float* dw_next, float* dw_post, float* dgate) {
+                                                              const float* w_post, const float* gate, float* dw_next,
+                                                              float* dw_post, float* dgate) {
     __shared__ float sums[8][32];
-    float* out = blockIdx.y == 0 ? dw_next : blockIdx.y == 1 ? dw_post : dgate;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    const bool next = blockIdx.y == 0;
     pdl_wait();
-    if (!out) return;
+    if (next ? !dw_next : !dw_post && !dgate) return;
     const int each = (n + 7) / 8, i1 = min(n, (w + 1) * each);
     float s = 0.f;
     if (c < D) {
 #pragma unroll 8
-        for (int i = w * each; i < i1; ++i) s += __ldg(part + ((size_t)i * 3 + blockIdx.y) * D + c);
+        for (int i = w * each; i < i1; ++i) s += __ldg(part + ((size_t)i * 2 + blockIdx.y) * D + c);
     }
     sums[w][lane] = s;
     __syncthreads();
-    if (w == 0 && c < D) {
+    if (w > 0 || c >= D) return;
 #pragma unroll
-        for (int i = 1; i < 8; ++i) s += sums[i][lane];
-        out[c] = s;
+    for (int i = 1; i < 8; ++i) s += sums[i][lane];
+    if (next) {
+        dw_next[c] = s;
+    } else {
+        if (dw_post) dw_post[c] = gate ? s * __ldg(gate + c) : s;
+        if (dgate) dgate[c] = w_post ? s * __ldg(w_post + c) : s;
     }
 }
 
-// Threads per token and tokens per block for rows of n packs per thread-iteration.
+// Threads per token, tokens per block and bytes of a row's slot.
 struct NormShape {
-    int group, groups;
-    NormShape(int D, int per_thread) {
+    int group, groups, pitch;
+    NormShape(int D, int per_thread, size_t elem, bool wide) {
         group = ((D + per_thread - 1) / per_thread + 31) / 32 * 32;
         groups = group >= kNormThreads ? 1 : kNormThreads / group;
         if (groups > kMaxGroups) groups = kMaxGroups;
+        pitch = (int)((D * elem + 15) / 16 * 16) + (wide ? 0 : 16);
     }
     int blocks(int T, int most) const {
         const int n = (T + groups - 1) / groups;
@@ -424,65 +466,60 @@ struct NormShape {
     }
 };
 
-template <typename T, int V, int ITER, int STAGES, int THREADS>
+template <typename T, int N, int STAGES, int THREADS, bool WIDE>
 cudaError_t run_norm(NormArgs a, cudaStream_t s) {
-    auto kernel = block_norm_kernel<T, V, ITER, STAGES, THREADS>;
-    const NormShape n(a.D, V * ITER);
-    const size_t smem = (size_t)n.groups * (256 + STAGES * 2 * a.D * sizeof(T));
+    auto kernel = block_norm_kernel<T, N, STAGES, THREADS, WIDE>;
+    const NormShape n(a.D, N, sizeof(T), WIDE);
     static std::atomic<uint64_t> set{0};
     if (!once_per_device(set, [&] {
             return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic) == cudaSuccess;
         }))
         return cudaErrorUnknown;
     a.group = n.group;
-    const int per_sm = THREADS > 512 ? 1 : n.group * n.groups > kNormThreads ? 2 : 3;      // as their registers allow
-    return launch_pdl(kernel, dim3(n.blocks(a.T, device_sm_count() * per_sm)), dim3(n.group * n.groups), smem, s, a);
+    a.pitch = n.pitch;
+    const int per_sm = THREADS > 512 ? 1 : 2;
+    return launch_pdl(kernel, dim3(n.blocks(a.T, device_sm_count() * per_sm)), dim3(n.group * n.groups),
+                      (size_t)n.groups * (kSumFloats * 4 + STAGES * 2 * n.pitch), s, a);
 }
-template <typename T, int V, int ITER, int STAGES, int THREADS, bool SMEM>
+template <typename T, int N, int STAGES, int THREADS, bool SMEM, bool WIDE>
 cudaError_t run_norm_backward(NormGradArgs a, int* blocks, cudaStream_t s) {
-    auto kernel = block_norm_backward_kernel<T, V, ITER, STAGES, THREADS, SMEM>;
-    const NormShape n(a.D, V * ITER);
-    const size_t smem = (SMEM || n.groups > 1 ? (size_t)3 * a.D * 4 : 0) +
-                        (size_t)n.groups * (768 + STAGES * 4 * a.D * sizeof(T));
+    auto kernel = block_norm_backward_kernel<T, N, STAGES, THREADS, SMEM, WIDE>;
+    const NormShape n(a.D, N, sizeof(T), WIDE);
     static std::atomic<uint64_t> set{0};
     if (!once_per_device(set, [&] {
             return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic) == cudaSuccess;
         }))
         return cudaErrorUnknown;
     a.group = n.group;
+    a.pitch = n.pitch;
     const int sms = device_sm_count() < kNormParts / 2 ? device_sm_count() : kNormParts / 2;
     *blocks = n.blocks(a.T, THREADS == kNormThreads ? 2 * sms : sms);
-    return launch_pdl(kernel, dim3(*blocks), dim3(n.group * n.groups), smem, s, a);
+    const size_t sums = SMEM || n.groups > 1 ? (size_t)(2 * a.D + 3) / 4 * 16 : 0;
+    return launch_pdl(kernel, dim3(*blocks), dim3(n.group * n.groups),
+                      sums + (size_t)n.groups * (kSumFloats * 4 + STAGES * 4 * n.pitch), s, a);
 }
 
-// Rows up to 4,096 elements keep their sums over tokens in registers (8 of each
-// per thread with 16-bit types, 4 with fp32); wider ones, and single elements
-// where the rows are not of 16-byte packs, as the limits of threads and
-// registers allow.
-template <typename T>
-cudaError_t pick_norm(const NormArgs& a, bool wide, cudaStream_t s) {
-    constexpr int V = 16 / sizeof(T);
-    if (!wide) {
-        if (a.D <= 2048) return run_norm<T, 1, 4, 0, 512>(a, s);
-        return run_norm<T, 1, 8, 0, 1024>(a, s);
-    }
-    if (a.D <= 512 * V) return run_norm<T, V, 1, 3, 512>(a, s);
-    if (a.D <= 1024 * V) return run_norm<T, V, 1, 3, 1024>(a, s);
-    return run_norm<T, V, sizeof(T) == 4 ? 2 : 1, 3, 1024>(a, s);
+// A thread has 16 bytes of a row (twice that for fp32 rows beyond 4,096).  Blocks
+// of 384 threads leave room for two per SM with the sums over tokens in
+// registers; beyond 4,096 elements those go to shared memory.
+template <typename T, bool WIDE>
+cudaError_t pick_norm(const NormArgs& a, cudaStream_t s) {
+    constexpr int N = 16 / sizeof(T);
+    if (a.D <= 512 * N) return run_norm<T, N, 3, 512, WIDE>(a, s);
+    if (a.D <= 1024 * N) return run_norm<T, N, 3, 1024, WIDE>(a, s);
+    return run_norm<T, 8, 3, 1024, WIDE>(a, s);
 }
-template <typename T>
-cudaError_t pick_norm_backward(const NormGradArgs& a, bool wide, int* blocks, cudaStream_t s) {
-    constexpr int V = 16 / sizeof(T);
-    if (!wide) {
-        if (a.D <= 4 * kNormThreads) return run_norm_backward<T, 1, 4, 0, kNormThreads, false>(a, blocks, s);
-        if (a.D <= 2048) return run_norm_backward<T, 1, 4, 0, 512, false>(a, blocks, s);
-        return run_norm_backward<T, 1, 8, 0, 1024, true>(a, blocks, s);
+template <typename T, bool WIDE>
+cudaError_t pick_norm_backward(const NormGradArgs& a, int* blocks, cudaStream_t s) {
+    constexpr int N = 16 / sizeof(T);
+    if (a.D <= kNormThreads * N) return run_norm_backward<T, N, 3, kNormThreads, false, WIDE>(a, blocks, s);
+    if (a.D <= 512 * N) return run_norm_backward<T, N, 3, 512, false, WIDE>(a, blocks, s);
+    if constexpr (N == 8) {
+        return run_norm_backward<T, N, 2, 1024, true, WIDE>(a, blocks, s);
+    } else {
+        if (a.D <= 1024 * N) return run_norm_backward<T, N, 3, 1024, false, WIDE>(a, blocks, s);
+        return run_norm_backward<T, 8, 1, 1024, true, WIDE>(a, blocks, s);
     }
-    if (a.D <= kNormThreads * V) return run_norm_backward<T, V, 1, 3, kNormThreads, false>(a, blocks, s);
-    if (a.D <= 512 * V) return run_norm_backward<T, V, 1, 3, 512, false>(a, blocks, s);
-    if constexpr (sizeof(T) == 2) return run_norm_backward<T, V, 1, 2, 1024, true>(a, blocks, s);
-    else if (a.D <= 1024 * V) return run_norm_backward<T, V, 1, 2, 1024, false>(a, blocks, s);
-    else return run_norm_backward<T, V, 2, 0, 1024, true>(a, blocks, s);
 }
 
 moe_status norm_shapes(int T, int D) { return ops_shapes(T, 1, D); }
@@ -495,7 +532,7 @@ bool gate_ok(const float* gate, int mode) {
 // |v| < infinity, and not NaN
 bool finite(float v) { return v - v == 0.f; }
 
-size_t norm_ws_bytes(int T, int D) { return (size_t)(T < kNormParts ? T : kNormParts) * 3 * D * 4 + 256; }
+size_t norm_ws_bytes(int T, int D) { return (size_t)(T < kNormParts ? T : kNormParts) * 2 * D * 4 + 256; }
 
 }  // namespace
 }  // namespace moe
@@ -520,8 +557,12 @@ extern "C" moe_status moe_block_norm(const void* y, const void* residual, const 
     const bool wide = (D * es) % 16 == 0 && ops_aligned(y, 16) && ops_aligned(residual, 16) && ops_aligned(x_out, 16) &&
                       ops_aligned(normed, 16) && ops_aligned(w_post, 16) && ops_aligned(w_next, 16) &&
                       (gate_mode != MOE_GATE_CHANNEL || ops_aligned(gate, 16));
-    const NormArgs a{y, residual, gate, gate_mode, alpha, w_post, w_next, eps, T, D, 0, x_out, normed, rstd_post, rstd_next};
-    return with_dtype(dtype, [&](auto e) { return ops_status(pick_norm<decltype(e)>(a, wide, (cudaStream_t)stream)); });
+    const NormArgs a{y, residual, gate, gate_mode, alpha, w_post, w_next, eps, T, D, 0, 0, x_out, normed, rstd_post, rstd_next};
+    cudaStream_t s = (cudaStream_t)stream;
+    return with_dtype(dtype, [&](auto e) {
+        using Tp = decltype(e);
+        return ops_status(wide ? pick_norm<Tp, true>(a, s) : pick_norm<Tp, false>(a, s));
+    });
 }
 
 extern "C" size_t moe_block_norm_backward_workspace_size(int T, int D) {
@@ -564,12 +605,17 @@ extern "C" moe_status moe_block_norm_backward(const void* dx_out, const void* dn
                       ops_aligned(x_out, 16) && ops_aligned(y, 16) && ops_aligned(dy, 16) &&
                       ops_aligned(dresidual, 16) && ops_aligned(w_post, 16) && ops_aligned(w_next, 16) &&
                       (gate_mode != MOE_GATE_CHANNEL || ops_aligned(gate, 16));
+    const bool per_token = gate_mode == MOE_GATE_TOKEN;
     const NormGradArgs a{dx_out, w_next ? dnormed : nullptr, w_next ? x_out : nullptr, w_post || dgate ? y : nullptr,
-                         gate, gate_mode, alpha, w_post, rstd_post, w_next, rstd_next, T, D, 0, dy, dresidual, dgate,
-                         dw_post, dw_next, static_cast<float*>(ws)};
+                         gate, gate_mode, alpha, w_post, rstd_post, w_next, rstd_next, T, D, 0, 0, dy, dresidual,
+                         per_token ? dgate : nullptr, dw_next != nullptr, dw_post || dgate_cols,
+                         static_cast<float*>(ws)};
     int blocks = 0;
-    st = with_dtype(dtype, [&](auto e) { return ops_status(pick_norm_backward<decltype(e)>(a, wide, &blocks, s)); });
+    st = with_dtype(dtype, [&](auto e) {
+        using Tp = decltype(e);
+        return ops_status(wide ? pick_norm_backward<Tp, true>(a, &blocks, s) : pick_norm_backward<Tp, false>(a, &blocks, s));
+    });
     if (st != MOE_OK || (!dw_next && !dw_post && !dgate_cols)) return st;
-    return ops_status(launch_pdl(block_norm_join_kernel, dim3((D + 31) / 32, 3), dim3(256), 0, s,
-                                 (const float*)ws, blocks, D, dw_next, dw_post, dgate_cols));
+    return ops_status(launch_pdl(block_norm_join_kernel, dim3((D + 31) / 32, 2), dim3(256), 0, s, (const float*)ws, blocks,
+                                 D, w_post, per_token ? nullptr : gate, dw_next, dw_post, dgate_cols));
 }
