@@ -79,6 +79,15 @@ MOE_DEVINL float dot(const float (&a)[N], const float (&b)[N]) {
     return s0 + s1;
 }
 
+// v as it reads back after a store as T
+template <typename T, int N>
+MOE_DEVINL void round_stored(float (&v)[N]) {
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) unpack_word(T{}, pack_word(T{}, v + i), v + i);
+    }
+}
+
 // A group's threads, and sums over them: the same bits in every thread, formed
 // in a fixed order (lanes, then warps).  buf: [2][4][32] floats of this group;
 // parity alternates from call to call, so one barrier per call is enough.
@@ -114,7 +123,9 @@ struct Group {
             if (lane % 8 == 0) b[rank / 32 * 4 + lane / 8] = v;
             sync();
             v = 0.f;
-            for (int w = lane % 8; w < size / 32; w += 8) v += b[w * 4 + lane / 8];
+#pragma unroll
+            for (int w = 0; w < 32; w += 8)
+                if (w * 32 < size && lane % 8 + w < size / 32) v += b[(lane % 8 + w) * 4 + lane / 8];
 #pragma unroll
             for (int o = 4; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         }
@@ -157,35 +168,38 @@ struct Cols {
     }
 };
 
-// The rows of a group's coming tokens, STAGES tokens ahead in shared memory.
-template <typename T, int N, int ROWS, int STAGES, bool WIDE>
+// The rows of a group's coming tokens, STAGES tokens ahead in shared memory, out
+// of the ROWS matrices a.rows (null: not there).  Offsets into the [T][D]
+// matrices are bytes in 32 bits (at most 2^31).
+template <typename T, int N, int ROWS, int STAGES, bool WIDE, typename Args>
 struct Ring {
-    const T* src[ROWS];                         // null: no such row
+    const Args& a;
+    const Cols<T, N, WIDE>& col;
     char* ring;                                 // [STAGES][ROWS][pitch] of this group
-    int pitch, T_, stage = 0;
-    Cols<T, N, WIDE> col;
-    MOE_DEVINL char* slot(int st, int r) const { return ring + (st * ROWS + r) * pitch; }
+    int slot = 0;                               // offset in the ring of the token to read next, then to fetch into
     // bytes from the row's place in its slot to its first element
-    MOE_DEVINL int lead(int r, int t) const {
-        return WIDE ? 0 : (int)((uintptr_t)(src[r] + (size_t)t * col.D) & 15);
+    MOE_DEVINL int lead(int r, uint32_t at) const {
+        return WIDE ? 0 : (int)((uintptr_t)(static_cast<const char*>(a.rows[r]) + at) & 15);
     }
-    MOE_DEVINL void fetch(int t, int st) {
-        if (t < T_) {
+    // Fetch the token at offset `at`, if there is one.
+    MOE_DEVINL void fetch(uint32_t at, bool live) {
+        if (live) {
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) {
-                if (!src[r]) continue;
-                const T* row = src[r] + (size_t)t * col.D;
-                char* to = slot(st, r);
+                if (!a.rows[r]) continue;
+                const char* src = static_cast<const char*>(a.rows[r]);
+                char* to = ring + slot + r * a.pitch;
                 if constexpr (WIDE) {
 #pragma unroll
                     for (int i = 0; i < Cols<T, N, WIDE>::ITER; ++i)
-                        if (col.at(i) < col.D) cp_async16(to + col.at(i) * sizeof(T), row + col.at(i));
+                        if (col.at(i) < a.D)
+                            cp_async16(to + col.at(i) * sizeof(T), src + (at + col.at(i) * (uint32_t)sizeof(T)));
                 } else {
-                    const char* lo = reinterpret_cast<const char*>(src[r]);             // the buffer
-                    const char* hi = lo + (size_t)T_ * col.D * sizeof(T);
-                    const char* from = reinterpret_cast<const char*>(row) - lead(r, t);
-                    const int bytes = lead(r, t) + col.D * (int)sizeof(T);
-                    for (int j = col.rank * 16; j < bytes; j += col.size * 16) {
+                    const uint32_t row_bytes = a.D * (uint32_t)sizeof(T);
+                    const char *lo = src, *hi = lo + (size_t)a.T * row_bytes;           // the buffer
+                    const char* from = src + at - lead(r, at);
+                    const int bytes = lead(r, at) + (int)row_bytes;
+                    for (int j = col.rank * 16; j < bytes; j += a.group * 16) {
                         if (from + j >= lo && from + j + 16 <= hi) {
                             cp_async16(to + j, from + j);
                         } else {
@@ -198,27 +212,68 @@ struct Ring {
             }
         }
         cp_async_commit();
-    }
-    MOE_DEVINL void begin(int t0, int step) {
-#pragma unroll
-        for (int i = 0; i < STAGES; ++i) fetch(t0 + i * step, i);
+        slot = slot == (STAGES - 1) * ROWS * a.pitch ? 0 : slot + ROWS * a.pitch;
     }
     MOE_DEVINL void wait(const Group& grp) const {
         cp_async_wait<STAGES - 1>();
         if (!WIDE) grp.sync();
     }
-    MOE_DEVINL void read(int r, int t, float (&v)[N]) const {
-        col.load(reinterpret_cast<const T*>(slot(stage, r) + lead(r, t)), v);
-    }
-    // The group has read token t's rows: fetch those of a later token in their place.
-    MOE_DEVINL void refill(int t, int step) {
-        fetch(t + STAGES * step, stage);
-        stage = stage + 1 == STAGES ? 0 : stage + 1;
+    MOE_DEVINL void read(int r, uint32_t at, float (&v)[N]) const {
+        col.load(reinterpret_cast<const T*>(ring + slot + r * a.pitch + lead(r, at)), v);
     }
 };
 
+// A thread's factors of its columns: w_post times a channel gate, and w_next
+// (1 where absent).  Kept in shared memory, a thread's N values in packs of four
+// that neighbouring threads hold next to one another, or in registers.
+template <int N, bool KEPT>
+struct Factors {
+    float4* at;                                 // [2][N / 4][threads per token]
+    float reg[KEPT ? 2 : 1][KEPT ? N : 1];
+    int rank, size;
+    template <typename Col, typename Args>
+    MOE_DEVINL void make(const Col& col, const Args& a, bool write) {
+        float v[N], w[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = 1.f;
+        if (a.w_post) col.load(a.w_post, v);
+        if (a.gate_mode == MOE_GATE_CHANNEL) {
+            col.load(a.gate, w);
+            mul(v, v, w);
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) w[j] = 1.f;
+        if (a.w_next) col.load(a.w_next, w);
+        if constexpr (KEPT) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) reg[0][j] = v[j], reg[1][j] = w[j];
+        } else if (write) {
+#pragma unroll
+            for (int j = 0; j < N; j += 4) {
+                at[j / 4 * size + rank] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                at[(N / 4 + j / 4) * size + rank] = make_float4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+            }
+        }
+    }
+    MOE_DEVINL void get(int n, float (&v)[N]) const {
+        if constexpr (KEPT) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] = reg[n][j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; j += 4) {
+                const float4 q = at[(n * (N / 4) + j / 4) * size + rank];
+                v[j] = q.x, v[j + 1] = q.y, v[j + 2] = q.z, v[j + 3] = q.w;
+            }
+        }
+    }
+};
+
+template <typename T>
+MOE_DEVINL T* at_bytes(void* p, uint32_t at) { return reinterpret_cast<T*>(static_cast<char*>(p) + at); }
+
 struct NormArgs {
-    const void *y, *residual;
+    const void* rows[2];                        // y, residual or null
     const float* gate;
     int gate_mode;
     float alpha;
@@ -230,35 +285,36 @@ struct NormArgs {
 };
 
 template <typename T, int N, int STAGES, int THREADS, bool WIDE>
-__global__ void __launch_bounds__(THREADS) block_norm_kernel(NormArgs a) {
+__global__ void __launch_bounds__(THREADS) block_norm_kernel(const __grid_constant__ NormArgs a) {
     extern __shared__ __align__(16) float dyn[];        // sums, then rings, of every group
     const int groups = blockDim.x / a.group, g = threadIdx.x / a.group, rank = threadIdx.x % a.group;
     const int step = gridDim.x * groups, t0 = blockIdx.x * groups + g;
     Group grp{g, rank, a.group, dyn + g * kSumFloats};
     const Cols<T, N, WIDE> col{rank, a.group, a.D};
-    Ring<T, N, 2, STAGES, WIDE> in{{static_cast<const T*>(a.y), static_cast<const T*>(a.residual)},
-                                   reinterpret_cast<char*>(dyn + groups * kSumFloats) + g * STAGES * 2 * a.pitch,
-                                   a.pitch, a.T, 0, col};
+    Ring<T, N, 2, STAGES, WIDE, NormArgs> in{a, col,
+                                             reinterpret_cast<char*>(dyn + groups * kSumFloats + 2 * N * a.group) + g * STAGES * 2 * a.pitch};
+    const uint32_t skip = step * a.D * (uint32_t)sizeof(T);
+    uint32_t at = t0 * a.D * (uint32_t)sizeof(T);       // the token's offset in every matrix
     pdl_wait();
-    in.begin(t0, step);
-    // the columns' factors: w_post times a channel gate, and w_next
-    float gw[N], wn[N];
 #pragma unroll
-    for (int j = 0; j < N; ++j) gw[j] = wn[j] = 1.f;
-    if (a.w_post) col.load(a.w_post, gw);
-    if (a.gate_mode == MOE_GATE_CHANNEL) {
-        col.load(a.gate, wn);
-        mul(gw, gw, wn);
-    }
-    if (a.w_next) col.load(a.w_next, wn);
+    for (int i = 0; i < STAGES; ++i) in.fetch(at + i * skip, t0 + i * step < a.T);
+    Factors<N, false> fac;
+    fac.at = reinterpret_cast<float4*>(dyn + groups * kSumFloats);
+    fac.rank = rank;
+    fac.size = a.group;
+    fac.make(col, a, g == 0);
+    __syncthreads();
     const float inv = 1.f / a.D;
+    const bool per_token = a.gate_mode == MOE_GATE_TOKEN;
+    float gt = per_token && t0 < a.T ? __ldg(a.gate + t0) : 1.f;    // loaded a token ahead
     for (int t = t0; t < a.T; t += step) {
         float v[N], r[N];
-        float f = a.gate_mode == MOE_GATE_TOKEN ? __ldg(a.gate + t) : 1.f;
+        float f = gt;
+        if (per_token && t + step < a.T) gt = __ldg(a.gate + t + step);
         in.wait(grp);
-        in.read(0, t, v);
-        if (a.residual) {
-            in.read(1, t, r);
+        in.read(0, at, v);
+        if (a.rows[1]) {
+            in.read(1, at, r);
             mul(r, r, a.alpha);
         } else {
 #pragma unroll
@@ -269,26 +325,29 @@ __global__ void __launch_bounds__(THREADS) block_norm_kernel(NormArgs a) {
             if (a.rstd_post && rank == 0) a.rstd_post[t] = ry;
             f *= ry;
         }
-        mul(v, v, gw);
+        float w[N];
+        fac.get(0, w);
+        mul(v, v, w);
         fma(v, v, f, r);
-#pragma unroll
-        for (int j = 0; j < N; ++j) v[j] = as_stored<T>(v[j]);
-        if (a.x_out) col.store(static_cast<T*>(a.x_out) + (size_t)t * a.D, v);
+        round_stored<T>(v);
+        if (a.x_out) col.store(at_bytes<T>(a.x_out, at), v);
         if (a.w_next) {
             const float rx = rsqrtf(__fmaf_rn(grp.sum(dot(v, v)), inv, a.eps));
             if (a.rstd_next && rank == 0) a.rstd_next[t] = rx;
-            mul(v, v, wn);
+            fac.get(1, w);
+            mul(v, v, w);
             mul(v, v, rx);
-            col.store(static_cast<T*>(a.normed) + (size_t)t * a.D, v);
+            col.store(at_bytes<T>(a.normed, at), v);
         } else if (!WIDE) {
             grp.sync();                         // all of the group have read the token
         }
-        in.refill(t, step);
+        in.fetch(at + STAGES * skip, t + STAGES * step < a.T);
+        at += skip;
     }
 }
 
 struct NormGradArgs {
-    const void *dx_out, *dnormed, *x_out, *y;   // dnormed, x_out: null without w_next; y: null if it is not read
+    const void* rows[4];                        // x_out and dnormed (null without w_next), dx_out or null, y (null if not read)
     const float* gate;
     int gate_mode;
     float alpha;
@@ -308,7 +367,8 @@ struct NormGradArgs {
 //   SMEM: the sums over tokens are kept in shared memory, for rows too wide for
 //   the registers.
 template <typename T, int N, int STAGES, int THREADS, bool SMEM, bool WIDE>
-__global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 2 : 1) block_norm_backward_kernel(NormGradArgs a) {
+__global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 2 : 1) 
+    block_norm_backward_kernel(const __grid_constant__ NormGradArgs a) {
     extern __shared__ __align__(16) float dyn[];        // the groups' sums, [2][D] sums over tokens, the groups' rings
     const int groups = blockDim.x / a.group, g = threadIdx.x / a.group, rank = threadIdx.x % a.group;
     const int step = gridDim.x * groups, t0 = blockIdx.x * groups + g;
@@ -316,10 +376,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 2 : 1) bloc
     const Cols<T, N, WIDE> col{rank, a.group, a.D};
     float* sums = dyn + groups * kSumFloats;            // with SMEM or several groups
     const int sums_floats = SMEM || groups > 1 ? (2 * a.D + 3) / 4 * 4 : 0;
-    Ring<T, N, 4, STAGES, WIDE> in{{static_cast<const T*>(a.x_out), static_cast<const T*>(a.dnormed),
-                                    static_cast<const T*>(a.dx_out), static_cast<const T*>(a.y)},
-                                   reinterpret_cast<char*>(sums + sums_floats) + g * STAGES * 4 * a.pitch,
-                                   a.pitch, a.T, 0, col};
+    Ring<T, N, 4, STAGES, WIDE, NormGradArgs> in{a, col,
+                                                 reinterpret_cast<char*>(sums + sums_floats + (SMEM ? 0 : 2 * N * a.group)) + g * STAGES * 4 * a.pitch};
+    const uint32_t skip = step * a.D * (uint32_t)sizeof(T);
+    uint32_t at = t0 * a.D * (uint32_t)sizeof(T);
     constexpr int M = SMEM ? 2 : N;
     float s_next[M], s_gy[M];
 #pragma unroll
@@ -329,30 +389,35 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 2 : 1) bloc
         __syncthreads();
     }
     pdl_wait();
-    in.begin(t0, step);
-    float gw[N], wn[N];
 #pragma unroll
-    for (int j = 0; j < N; ++j) gw[j] = wn[j] = 1.f;
-    if (a.w_post) col.load(a.w_post, gw);
-    if (a.gate_mode == MOE_GATE_CHANNEL) {
-        col.load(a.gate, wn);
-        mul(gw, gw, wn);
-    }
-    if (a.w_next) col.load(a.w_next, wn);
+    for (int i = 0; i < STAGES; ++i) in.fetch(at + i * skip, t0 + i * step < a.T);
+    Factors<N, SMEM> fac;
+    fac.at = reinterpret_cast<float4*>(sums + sums_floats);
+    fac.rank = rank;
+    fac.size = a.group;
+    fac.make(col, a, g == 0);
+    __syncthreads();
     const float inv = 1.f / a.D;
+    float rx_next = 0.f, ry_next = 1.f, gt_next = 1.f;  // loaded a token ahead
+    auto scalars = [&](int t) {
+        if (t >= a.T) return;
+        if (a.w_next) rx_next = __ldg(a.rstd_next + t);
+        if (a.w_post) ry_next = __ldg(a.rstd_post + t);
+        if (a.gate_mode == MOE_GATE_TOKEN) gt_next = __ldg(a.gate + t);
+    };
+    scalars(t0);
     for (int t = t0; t < a.T; t += step) {
-        const float rx = a.w_next ? __ldg(a.rstd_next + t) : 0.f;
-        const float ry = a.w_post ? __ldg(a.rstd_post + t) : 1.f;
-        const float gt = a.gate_mode == MOE_GATE_TOKEN ? __ldg(a.gate + t) : 1.f;
-        float b[N], xh[N], yh[N], m[N];
+        const float rx = rx_next, ry = ry_next, gt = gt_next;
+        scalars(t + step);
+        float b[N], xh[N], yh[N], m[N], w[N];
         float s0 = 0.f, s1 = 0.f, s2 = 0.f;     // sums of xh u, q b, q xh
         in.wait(grp);
 #pragma unroll
         for (int j = 0; j < N; ++j) b[j] = xh[j] = yh[j] = 0.f;
-        if (a.dx_out) in.read(2, t, b);
+        if (a.rows[2]) in.read(2, at, b);
         if (a.w_next) {
-            in.read(0, t, xh);
-            in.read(1, t, m);
+            in.read(0, at, xh);
+            in.read(1, at, m);
             mul(xh, xh, rx);
             if constexpr (!SMEM) {
                 fma(s_next, m, xh, s_next);
@@ -362,26 +427,28 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 2 : 1) bloc
                 fma(acc, m, xh, acc);
                 col.store(sums, acc);
             }
-            mul(m, m, wn);                      // u
+            fac.get(1, w);
+            mul(m, m, w);                       // u
             s0 = dot(xh, m);
             fma(b, m, rx, b);
         }
-        if (a.y) {
-            in.read(3, t, yh);
+        if (a.rows[3]) {
+            in.read(3, at, yh);
             mul(yh, yh, ry);
-            mul(m, yh, gw);                     // q
+            fac.get(0, w);
+            mul(m, yh, w);                      // q
             s1 = dot(m, b);
             s2 = dot(m, xh);
         }
         grp.sum3(s0, s1, s2);
-        in.refill(t, step);
+        in.fetch(at + STAGES * skip, t + STAGES * step < a.T);  // all of the group have read the token
         const float rc1 = rx * s0 * inv, sq = __fmaf_rn(-rc1, s2, s1);
         const float c2 = a.w_post ? gt * sq * inv : 0.f;
         if (a.dgate && rank == 0) a.dgate[t] = sq;
         fma(b, xh, -rc1, b);                    // G
         if (a.dresidual) {
             mul(m, b, a.alpha);
-            col.store(static_cast<T*>(a.dresidual) + (size_t)t * a.D, m);
+            col.store(at_bytes<T>(a.dresidual, at), m);
         }
         mul(b, b, gt);
         if constexpr (!SMEM) {
@@ -391,10 +458,12 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 2 : 1) bloc
             fma(m, b, yh, m);
             col.store(sums + a.D, m);
         }
-        mul(b, b, gw);
+        fac.get(0, w);
+        mul(b, b, w);
         if (a.w_post) fma(b, yh, -c2, b);
         mul(b, b, ry);
-        col.store(static_cast<T*>(a.dy) + (size_t)t * a.D, b);
+        col.store(at_bytes<T>(a.dy, at), b);
+        at += skip;
     }
     // The block's sums: from the registers, or those of its groups added in order.
     float* part = a.part + (size_t)blockIdx.x * 2 * a.D;
@@ -479,7 +548,7 @@ cudaError_t run_norm(NormArgs a, cudaStream_t s) {
     a.pitch = n.pitch;
     const int per_sm = THREADS > 512 ? 1 : 2;
     return launch_pdl(kernel, dim3(n.blocks(a.T, device_sm_count() * per_sm)), dim3(n.group * n.groups),
-                      (size_t)n.groups * (kSumFloats * 4 + STAGES * 2 * n.pitch), s, a);
+                      (size_t)n.groups * (kSumFloats * 4 + STAGES * 2 * n.pitch) + (size_t)n.group * N * 8, s, a);
 }
 template <typename T, int N, int STAGES, int THREADS, bool SMEM, bool WIDE>
 cudaError_t run_norm_backward(NormGradArgs a, int* blocks, cudaStream_t s) {
@@ -496,7 +565,7 @@ cudaError_t run_norm_backward(NormGradArgs a, int* blocks, cudaStream_t s) {
     *blocks = n.blocks(a.T, THREADS == kNormThreads ? 2 * sms : sms);
     const size_t sums = SMEM || n.groups > 1 ? (size_t)(2 * a.D + 3) / 4 * 16 : 0;
     return launch_pdl(kernel, dim3(*blocks), dim3(n.group * n.groups),
-                      sums + (size_t)n.groups * (kSumFloats * 4 + STAGES * 4 * n.pitch), s, a);
+                      sums + (SMEM ? 0 : (size_t)n.group * N * 8) + (size_t)n.groups * (kSumFloats * 4 + STAGES * 4 * n.pitch), s, a);
 }
 
 // A thread has 16 bytes of a row (twice that for fp32 rows beyond 4,096).  Blocks
@@ -507,7 +576,7 @@ cudaError_t pick_norm(const NormArgs& a, cudaStream_t s) {
     constexpr int N = 16 / sizeof(T);
     if (a.D <= 512 * N) return run_norm<T, N, 3, 512, WIDE>(a, s);
     if (a.D <= 1024 * N) return run_norm<T, N, 3, 1024, WIDE>(a, s);
-    return run_norm<T, 8, 3, 1024, WIDE>(a, s);
+    return run_norm<T, 8, 2, 1024, WIDE>(a, s);
 }
 template <typename T, bool WIDE>
 cudaError_t pick_norm_backward(const NormGradArgs& a, int* blocks, cudaStream_t s) {
@@ -517,7 +586,7 @@ cudaError_t pick_norm_backward(const NormGradArgs& a, int* blocks, cudaStream_t 
     if constexpr (N == 8) {
         return run_norm_backward<T, N, 2, 1024, true, WIDE>(a, blocks, s);
     } else {
-        if (a.D <= 1024 * N) return run_norm_backward<T, N, 3, 1024, false, WIDE>(a, blocks, s);
+        if (a.D <= 1024 * N) return run_norm_backward<T, N, 2, 1024, false, WIDE>(a, blocks, s);
         return run_norm_backward<T, 8, 1, 1024, true, WIDE>(a, blocks, s);
     }
 }
@@ -557,7 +626,7 @@ extern "C" moe_status moe_block_norm(const void* y, const void* residual, const 
     const bool wide = (D * es) % 16 == 0 && ops_aligned(y, 16) && ops_aligned(residual, 16) && ops_aligned(x_out, 16) &&
                       ops_aligned(normed, 16) && ops_aligned(w_post, 16) && ops_aligned(w_next, 16) &&
                       (gate_mode != MOE_GATE_CHANNEL || ops_aligned(gate, 16));
-    const NormArgs a{y, residual, gate, gate_mode, alpha, w_post, w_next, eps, T, D, 0, 0, x_out, normed, rstd_post, rstd_next};
+    const NormArgs a{{y, residual}, gate, gate_mode, alpha, w_post, w_next, eps, T, D, 0, 0, x_out, normed, rstd_post, rstd_next};
     cudaStream_t s = (cudaStream_t)stream;
     return with_dtype(dtype, [&](auto e) {
         using Tp = decltype(e);
@@ -606,8 +675,7 @@ extern "C" moe_status moe_block_norm_backward(const void* dx_out, const void* dn
                       ops_aligned(dresidual, 16) && ops_aligned(w_post, 16) && ops_aligned(w_next, 16) &&
                       (gate_mode != MOE_GATE_CHANNEL || ops_aligned(gate, 16));
     const bool per_token = gate_mode == MOE_GATE_TOKEN;
-    const NormGradArgs a{dx_out, w_next ? dnormed : nullptr, w_next ? x_out : nullptr, w_post || dgate ? y : nullptr,
-                         gate, gate_mode, alpha, w_post, rstd_post, w_next, rstd_next, T, D, 0, 0, dy, dresidual,
+    const NormGradArgs a{{w_next ? x_out : nullptr, w_next ? dnormed : nullptr, dx_out, w_post || dgate ? y : nullptr}, gate, gate_mode, alpha, w_post, rstd_post, w_next, rstd_next, T, D, 0, 0, dy, dresidual,
                          per_token ? dgate : nullptr, dw_next != nullptr, dw_post || dgate_cols,
                          static_cast<float*>(ws)};
     int blocks = 0;
