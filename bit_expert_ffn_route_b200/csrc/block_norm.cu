@@ -136,13 +136,19 @@ struct Group {
 };
 constexpr int kSumFloats = 256;
 
+// How rows lie: they start anywhere (ANY), they are of whole 16-byte packs
+// (WIDE), or besides every thread of the group has all its columns and the call
+// has every operand but a token gate (FULL: no test of these in the token's path).
+enum { ANY, WIDE, FULL };
+
 // Thread `rank` of a group of `size` owns N elements of a row: packs of V, at
 // (i size + rank) V (V = 1: single elements of rows that start anywhere).
-template <typename T, int N, bool WIDE>
+template <typename T, int N, int KIND>
 struct Cols {
-    static constexpr int V = WIDE ? (N < 16 / (int)sizeof(T) ? N : 16 / (int)sizeof(T)) : 1, ITER = N / V;
+    static constexpr int V = KIND != ANY ? (N < 16 / (int)sizeof(T) ? N : 16 / (int)sizeof(T)) : 1, ITER = N / V;
     int rank, size, D;
     MOE_DEVINL int at(int i) const { return (i * size + rank) * V; }
+    MOE_DEVINL bool in(int i) const { return KIND == FULL || at(i) < D; }
     // Elements outside the row are zero.
     template <typename S>
     MOE_DEVINL void load(const S* p, float (&v)[N]) const {
@@ -151,7 +157,7 @@ struct Cols {
             float w[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) w[j] = 0.f;
-            if (at(i) < D) load_f32<S, V>(p + at(i), w);
+            if (in(i)) load_f32<S, V>(p + at(i), w);
 #pragma unroll
             for (int j = 0; j < V; ++j) v[i * V + j] = w[j];
         }
@@ -163,7 +169,7 @@ struct Cols {
             float w[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) w[j] = v[i * V + j];
-            if (at(i) < D) store_f32<S, V>(p + at(i), w);
+            if (in(i)) store_f32<S, V>(p + at(i), w);
         }
     }
 };
@@ -171,28 +177,28 @@ struct Cols {
 // The rows of a group's coming tokens, STAGES tokens ahead in shared memory, out
 // of the ROWS matrices a.rows (null: not there).  Offsets into the [T][D]
 // matrices are bytes in 32 bits (at most 2^31).
-template <typename T, int N, int ROWS, int STAGES, bool WIDE, typename Args>
+template <typename T, int N, int ROWS, int STAGES, int KIND, typename Args>
 struct Ring {
     const Args& a;
-    const Cols<T, N, WIDE>& col;
+    const Cols<T, N, KIND>& col;
     char* ring;                                 // [STAGES][ROWS][pitch] of this group
     int slot = 0;                               // offset in the ring of the token to read next, then to fetch into
     // bytes from the row's place in its slot to its first element
     MOE_DEVINL int lead(int r, uint32_t at) const {
-        return WIDE ? 0 : (int)((uintptr_t)(static_cast<const char*>(a.rows[r]) + at) & 15);
+        return KIND != ANY ? 0 : (int)((uintptr_t)(static_cast<const char*>(a.rows[r]) + at) & 15);
     }
     // Fetch the token at offset `at`, if there is one.
     MOE_DEVINL void fetch(uint32_t at, bool live) {
         if (live) {
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) {
-                if (!a.rows[r]) continue;
+                if (KIND != FULL && !a.rows[r]) continue;
                 const char* src = static_cast<const char*>(a.rows[r]);
                 char* to = ring + slot + r * a.pitch;
-                if constexpr (WIDE) {
+                if constexpr (KIND != ANY) {
 #pragma unroll
-                    for (int i = 0; i < Cols<T, N, WIDE>::ITER; ++i)
-                        if (col.at(i) < a.D)
+                    for (int i = 0; i < Cols<T, N, KIND>::ITER; ++i)
+                        if (col.in(i))
                             cp_async16(to + col.at(i) * sizeof(T), src + (at + col.at(i) * (uint32_t)sizeof(T)));
                 } else {
                     const uint32_t row_bytes = a.D * (uint32_t)sizeof(T);
@@ -216,7 +222,7 @@ struct Ring {
     }
     MOE_DEVINL void wait(const Group& grp) const {
         cp_async_wait<STAGES - 1>();
-        if (!WIDE) grp.sync();
+        if (KIND == ANY) grp.sync();
     }
     MOE_DEVINL void read(int r, uint32_t at, float (&v)[N]) const {
         col.load(reinterpret_cast<const T*>(ring + slot + r * a.pitch + lead(r, at)), v);
@@ -284,14 +290,15 @@ struct NormArgs {
     float *rstd_post, *rstd_next;
 };
 
-template <typename T, int N, int STAGES, int THREADS, bool WIDE>
-__global__ void __launch_bounds__(THREADS) block_norm_kernel(const __grid_constant__ NormArgs a) {
+template <typename T, int N, int STAGES, int THREADS, int KIND>
+__global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 3 : 1)
+    block_norm_kernel(const __grid_constant__ NormArgs a) {
     extern __shared__ __align__(16) float dyn[];        // sums, then rings, of every group
     const int groups = blockDim.x / a.group, g = threadIdx.x / a.group, rank = threadIdx.x % a.group;
     const int step = gridDim.x * groups, t0 = blockIdx.x * groups + g;
     Group grp{g, rank, a.group, dyn + g * kSumFloats};
-    const Cols<T, N, WIDE> col{rank, a.group, a.D};
-    Ring<T, N, 2, STAGES, WIDE, NormArgs> in{a, col,
+    const Cols<T, N, KIND> col{rank, a.group, a.D};
+    Ring<T, N, 2, STAGES, KIND, NormArgs> in{a, col,
                                              reinterpret_cast<char*>(dyn + groups * kSumFloats + 2 * N * a.group) + g * STAGES * 2 * a.pitch};
     const uint32_t skip = step * a.D * (uint32_t)sizeof(T);
     uint32_t at = t0 * a.D * (uint32_t)sizeof(T);       // the token's offset in every matrix
@@ -305,7 +312,8 @@ __global__ void __launch_bounds__(THREADS) block_norm_kernel(const __grid_consta
     fac.make(col, a, g == 0);
     __syncthreads();
     const float inv = 1.f / a.D;
-    const bool per_token = a.gate_mode == MOE_GATE_TOKEN;
+    const bool per_token = KIND != FULL && a.gate_mode == MOE_GATE_TOKEN;
+    const bool post = KIND == FULL || a.w_post, next = KIND == FULL || a.w_next;
     float gt = per_token && t0 < a.T ? __ldg(a.gate + t0) : 1.f;    // loaded a token ahead
     for (int t = t0; t < a.T; t += step) {
         float v[N], r[N];
@@ -313,14 +321,14 @@ __global__ void __launch_bounds__(THREADS) block_norm_kernel(const __grid_consta
         if (per_token && t + step < a.T) gt = __ldg(a.gate + t + step);
         in.wait(grp);
         in.read(0, at, v);
-        if (a.rows[1]) {
+        if (KIND == FULL || a.rows[1]) {
             in.read(1, at, r);
             mul(r, r, a.alpha);
         } else {
 #pragma unroll
             for (int j = 0; j < N; ++j) r[j] = 0.f;
         }
-        if (a.w_post) {
+        if (post) {
             const float ry = rsqrtf(__fmaf_rn(grp.sum(dot(v, v)), inv, a.eps));
             if (a.rstd_post && rank == 0) a.rstd_post[t] = ry;
             f *= ry;
@@ -330,15 +338,15 @@ __global__ void __launch_bounds__(THREADS) block_norm_kernel(const __grid_consta
         mul(v, v, w);
         fma(v, v, f, r);
         round_stored<T>(v);
-        if (a.x_out) col.store(at_bytes<T>(a.x_out, at), v);
-        if (a.w_next) {
+        if (KIND == FULL || a.x_out) col.store(at_bytes<T>(a.x_out, at), v);
+        if (next) {
             const float rx = rsqrtf(__fmaf_rn(grp.sum(dot(v, v)), inv, a.eps));
             if (a.rstd_next && rank == 0) a.rstd_next[t] = rx;
             fac.get(1, w);
             mul(v, v, w);
             mul(v, v, rx);
             col.store(at_bytes<T>(a.normed, at), v);
-        } else if (!WIDE) {
+        } else if (KIND == ANY) {
             grp.sync();                         // all of the group have read the token
         }
         in.fetch(at + STAGES * skip, t + STAGES * step < a.T);
@@ -366,17 +374,17 @@ struct NormGradArgs {
 // for all tokens, so both their gradients come from the sums of G yh.
 //   SMEM: the sums over tokens are kept in shared memory, for rows too wide for
 //   the registers.
-template <typename T, int N, int STAGES, int THREADS, bool SMEM, bool WIDE>
+template <typename T, int N, int STAGES, int THREADS, bool SMEM, int KIND>
 __global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 2 : 1) 
     block_norm_backward_kernel(const __grid_constant__ NormGradArgs a) {
     extern __shared__ __align__(16) float dyn[];        // the groups' sums, [2][D] sums over tokens, the groups' rings
     const int groups = blockDim.x / a.group, g = threadIdx.x / a.group, rank = threadIdx.x % a.group;
     const int step = gridDim.x * groups, t0 = blockIdx.x * groups + g;
     Group grp{g, rank, a.group, dyn + g * kSumFloats};
-    const Cols<T, N, WIDE> col{rank, a.group, a.D};
+    const Cols<T, N, KIND> col{rank, a.group, a.D};
     float* sums = dyn + groups * kSumFloats;            // with SMEM or several groups
     const int sums_floats = SMEM || groups > 1 ? (2 * a.D + 3) / 4 * 4 : 0;
-    Ring<T, N, 4, STAGES, WIDE, NormGradArgs> in{a, col,
+    Ring<T, N, 4, STAGES, KIND, NormGradArgs> in{a, col,
                                                  reinterpret_cast<char*>(sums + sums_floats + (SMEM ? 0 : 2 * N * a.group)) + g * STAGES * 4 * a.pitch};
     const uint32_t skip = step * a.D * (uint32_t)sizeof(T);
     uint32_t at = t0 * a.D * (uint32_t)sizeof(T);
@@ -398,12 +406,14 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 2 : 1)
     fac.make(col, a, g == 0);
     __syncthreads();
     const float inv = 1.f / a.D;
+    const bool next = KIND == FULL || a.w_next, post = KIND == FULL || a.w_post;
+    const bool per_token = KIND != FULL && a.gate_mode == MOE_GATE_TOKEN;
     float rx_next = 0.f, ry_next = 1.f, gt_next = 1.f;  // loaded a token ahead
     auto scalars = [&](int t) {
         if (t >= a.T) return;
-        if (a.w_next) rx_next = __ldg(a.rstd_next + t);
-        if (a.w_post) ry_next = __ldg(a.rstd_post + t);
-        if (a.gate_mode == MOE_GATE_TOKEN) gt_next = __ldg(a.gate + t);
+        if (next) rx_next = __ldg(a.rstd_next + t);
+        if (post) ry_next = __ldg(a.rstd_post + t);
+        if (per_token) gt_next = __ldg(a.gate + t);
     };
     scalars(t0);
     for (int t = t0; t < a.T; t += step) {
@@ -414,8 +424,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 2 : 1)
         in.wait(grp);
 #pragma unroll
         for (int j = 0; j < N; ++j) b[j] = xh[j] = yh[j] = 0.f;
-        if (a.rows[2]) in.read(2, at, b);
-        if (a.w_next) {
+        if (KIND == FULL || a.rows[2]) in.read(2, at, b);
+        if (next) {
             in.read(0, at, xh);
             in.read(1, at, m);
             mul(xh, xh, rx);
@@ -432,7 +442,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 2 : 1)
             s0 = dot(xh, m);
             fma(b, m, rx, b);
         }
-        if (a.rows[3]) {
+        if (KIND == FULL || a.rows[3]) {
             in.read(3, at, yh);
             mul(yh, yh, ry);
             fac.get(0, w);
@@ -443,14 +453,14 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 2 : 1)
         grp.sum3(s0, s1, s2);
         in.fetch(at + STAGES * skip, t + STAGES * step < a.T);  // all of the group have read the token
         const float rc1 = rx * s0 * inv, sq = __fmaf_rn(-rc1, s2, s1);
-        const float c2 = a.w_post ? gt * sq * inv : 0.f;
-        if (a.dgate && rank == 0) a.dgate[t] = sq;
+        const float c2 = post ? gt * sq * inv : 0.f;
+        if (KIND != FULL && a.dgate && rank == 0) a.dgate[t] = sq;
         fma(b, xh, -rc1, b);                    // G
-        if (a.dresidual) {
+        if (KIND == FULL || a.dresidual) {
             mul(m, b, a.alpha);
             col.store(at_bytes<T>(a.dresidual, at), m);
         }
-        mul(b, b, gt);
+        if (per_token) mul(b, b, gt);
         if constexpr (!SMEM) {
             fma(s_gy, b, yh, s_gy);
         } else if (a.want_post) {
@@ -460,7 +470,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 2 : 1)
         }
         fac.get(0, w);
         mul(b, b, w);
-        if (a.w_post) fma(b, yh, -c2, b);
+        if (post) fma(b, yh, -c2, b);
         mul(b, b, ry);
         col.store(at_bytes<T>(a.dy, at), b);
         at += skip;
@@ -491,27 +501,27 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 2 : 1)
     }
 }
 
-// Column sums of the blocks' partials: 32 columns per block, an eighth of the
-// partials per warp, the eighths added in order.
-__global__ void __launch_bounds__(256) block_norm_join_kernel(const float* __restrict__ part, int n, int D,
+// Column sums of the blocks' partials: 32 columns per block, each of its 32 warps
+// a share of the partials, the shares added in order.
+__global__ void __launch_bounds__(1024) block_norm_join_kernel(const float* __restrict__ part, int n, int D,
                                                               const float* w_post, const float* gate, float* dw_next,
                                                               float* dw_post, float* dgate) {
-    __shared__ float sums[8][32];
+    __shared__ float sums[32][32];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     const bool next = blockIdx.y == 0;
     pdl_wait();
     if (next ? !dw_next : !dw_post && !dgate) return;
-    const int each = (n + 7) / 8, i1 = min(n, (w + 1) * each);
+    const int each = (n + 31) / 32, i1 = min(n, (w + 1) * each);
     float s = 0.f;
     if (c < D) {
-#pragma unroll 8
+#pragma unroll 10
         for (int i = w * each; i < i1; ++i) s += __ldg(part + ((size_t)i * 2 + blockIdx.y) * D + c);
     }
     sums[w][lane] = s;
     __syncthreads();
     if (w > 0 || c >= D) return;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += sums[i][lane];
+    for (int i = 1; i < 32; ++i) s += sums[i][lane];
     if (next) {
         dw_next[c] = s;
     } else {
@@ -535,10 +545,10 @@ struct NormShape {
     }
 };
 
-template <typename T, int N, int STAGES, int THREADS, bool WIDE>
+template <typename T, int N, int STAGES, int THREADS, int KIND>
 cudaError_t run_norm(NormArgs a, cudaStream_t s) {
-    auto kernel = block_norm_kernel<T, N, STAGES, THREADS, WIDE>;
-    const NormShape n(a.D, N, sizeof(T), WIDE);
+    auto kernel = block_norm_kernel<T, N, STAGES, THREADS, KIND>;
+    const NormShape n(a.D, N, sizeof(T), KIND != ANY);
     static std::atomic<uint64_t> set{0};
     if (!once_per_device(set, [&] {
             return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic) == cudaSuccess;
@@ -546,14 +556,14 @@ cudaError_t run_norm(NormArgs a, cudaStream_t s) {
         return cudaErrorUnknown;
     a.group = n.group;
     a.pitch = n.pitch;
-    const int per_sm = THREADS > 512 ? 1 : 2;
+    const int per_sm = THREADS > 512 ? 1 : THREADS == kNormThreads ? 3 : 2;
     return launch_pdl(kernel, dim3(n.blocks(a.T, device_sm_count() * per_sm)), dim3(n.group * n.groups),
                       (size_t)n.groups * (kSumFloats * 4 + STAGES * 2 * n.pitch) + (size_t)n.group * N * 8, s, a);
 }
-template <typename T, int N, int STAGES, int THREADS, bool SMEM, bool WIDE>
+template <typename T, int N, int STAGES, int THREADS, bool SMEM, int KIND>
 cudaError_t run_norm_backward(NormGradArgs a, int* blocks, cudaStream_t s) {
-    auto kernel = block_norm_backward_kernel<T, N, STAGES, THREADS, SMEM, WIDE>;
-    const NormShape n(a.D, N, sizeof(T), WIDE);
+    auto kernel = block_norm_backward_kernel<T, N, STAGES, THREADS, SMEM, KIND>;
+    const NormShape n(a.D, N, sizeof(T), KIND != ANY);
     static std::atomic<uint64_t> set{0};
     if (!once_per_device(set, [&] {
             return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic) == cudaSuccess;
@@ -571,25 +581,32 @@ cudaError_t run_norm_backward(NormGradArgs a, int* blocks, cudaStream_t s) {
 // A thread has 16 bytes of a row (twice that for fp32 rows beyond 4,096).  Blocks
 // of 384 threads leave room for two per SM with the sums over tokens in
 // registers; beyond 4,096 elements those go to shared memory.
-template <typename T, bool WIDE>
+template <typename T, int KIND>
 cudaError_t pick_norm(const NormArgs& a, cudaStream_t s) {
     constexpr int N = 16 / sizeof(T);
-    if (a.D <= 512 * N) return run_norm<T, N, 3, 512, WIDE>(a, s);
-    if (a.D <= 1024 * N) return run_norm<T, N, 3, 1024, WIDE>(a, s);
-    return run_norm<T, 8, 2, 1024, WIDE>(a, s);
+    if (a.D <= kNormThreads * N) return run_norm<T, N, 3, kNormThreads, KIND>(a, s);
+    if (a.D <= 512 * N) return run_norm<T, N, 3, 512, KIND>(a, s);
+    if constexpr (N == 4) {
+        if (a.D > 1024 * N) return run_norm<T, 8, 2, 1024, KIND>(a, s);
+    }
+    return run_norm<T, N, 3, 1024, KIND>(a, s);
 }
-template <typename T, bool WIDE>
+template <typename T, int KIND>
 cudaError_t pick_norm_backward(const NormGradArgs& a, int* blocks, cudaStream_t s) {
     constexpr int N = 16 / sizeof(T);
-    if (a.D <= kNormThreads * N) return run_norm_backward<T, N, 3, kNormThreads, false, WIDE>(a, blocks, s);
-    if (a.D <= 512 * N) return run_norm_backward<T, N, 3, 512, false, WIDE>(a, blocks, s);
+    if (a.D <= kNormThreads * N) return run_norm_backward<T, N, 3, kNormThreads, false, KIND>(a, blocks, s);
+    if (a.D <= 512 * N) return run_norm_backward<T, N, 3, 512, false, KIND>(a, blocks, s);
     if constexpr (N == 8) {
-        return run_norm_backward<T, N, 2, 1024, true, WIDE>(a, blocks, s);
+        return run_norm_backward<T, N, 2, 1024, true, KIND>(a, blocks, s);
     } else {
-        if (a.D <= 1024 * N) return run_norm_backward<T, N, 2, 1024, false, WIDE>(a, blocks, s);
-        return run_norm_backward<T, 8, 1, 1024, true, WIDE>(a, blocks, s);
+        if (a.D <= 1024 * N) return run_norm_backward<T, N, 2, 1024, false, KIND>(a, blocks, s);
+        return run_norm_backward<T, 8, 1, 1024, true, KIND>(a, blocks, s);
     }
 }
+
+// Whether every thread of the groups has all its columns: D a multiple of 32 N,
+// with the N that the D takes above.
+bool whole_groups(int D, size_t elem) { return D % (elem == 4 && D <= 4096 ? 128 : 256) == 0; }
 
 moe_status norm_shapes(int T, int D) { return ops_shapes(T, 1, D); }
 
@@ -626,11 +643,12 @@ extern "C" moe_status moe_block_norm(const void* y, const void* residual, const 
     const bool wide = (D * es) % 16 == 0 && ops_aligned(y, 16) && ops_aligned(residual, 16) && ops_aligned(x_out, 16) &&
                       ops_aligned(normed, 16) && ops_aligned(w_post, 16) && ops_aligned(w_next, 16) &&
                       (gate_mode != MOE_GATE_CHANNEL || ops_aligned(gate, 16));
+    const bool full = wide && whole_groups(D, es) && residual && w_post && w_next && x_out && gate_mode != MOE_GATE_TOKEN;
     const NormArgs a{{y, residual}, gate, gate_mode, alpha, w_post, w_next, eps, T, D, 0, 0, x_out, normed, rstd_post, rstd_next};
     cudaStream_t s = (cudaStream_t)stream;
     return with_dtype(dtype, [&](auto e) {
         using Tp = decltype(e);
-        return ops_status(wide ? pick_norm<Tp, true>(a, s) : pick_norm<Tp, false>(a, s));
+        return ops_status(full ? pick_norm<Tp, FULL>(a, s) : wide ? pick_norm<Tp, WIDE>(a, s) : pick_norm<Tp, ANY>(a, s));
     });
 }
 
@@ -675,15 +693,18 @@ extern "C" moe_status moe_block_norm_backward(const void* dx_out, const void* dn
                       ops_aligned(dresidual, 16) && ops_aligned(w_post, 16) && ops_aligned(w_next, 16) &&
                       (gate_mode != MOE_GATE_CHANNEL || ops_aligned(gate, 16));
     const bool per_token = gate_mode == MOE_GATE_TOKEN;
+    const bool full = wide && whole_groups(D, es) && dx_out && w_post && w_next && dresidual && !per_token;
     const NormGradArgs a{{w_next ? x_out : nullptr, w_next ? dnormed : nullptr, dx_out, w_post || dgate ? y : nullptr}, gate, gate_mode, alpha, w_post, rstd_post, w_next, rstd_next, T, D, 0, 0, dy, dresidual,
                          per_token ? dgate : nullptr, dw_next != nullptr, dw_post || dgate_cols,
                          static_cast<float*>(ws)};
     int blocks = 0;
     st = with_dtype(dtype, [&](auto e) {
         using Tp = decltype(e);
-        return ops_status(wide ? pick_norm_backward<Tp, true>(a, &blocks, s) : pick_norm_backward<Tp, false>(a, &blocks, s));
+        return ops_status(full   ? pick_norm_backward<Tp, FULL>(a, &blocks, s)
+                          : wide ? pick_norm_backward<Tp, WIDE>(a, &blocks, s)
+                                 : pick_norm_backward<Tp, ANY>(a, &blocks, s));
     });
     if (st != MOE_OK || (!dw_next && !dw_post && !dgate_cols)) return st;
-    return ops_status(launch_pdl(block_norm_join_kernel, dim3((D + 31) / 32, 2), dim3(256), 0, s, (const float*)ws, blocks,
+    return ops_status(launch_pdl(block_norm_join_kernel, dim3((D + 31) / 32, 2), dim3(1024), 0, s, (const float*)ws, blocks,
                                  D, w_post, per_token ? nullptr : gate, dw_next, dw_post, dgate_cols));
 }
