@@ -275,6 +275,10 @@ struct Factors {
     }
 };
 
+// The widest fp32 rows leave no shared memory for the factors.
+template <typename T>
+constexpr bool kept_factors(bool smem_sums) { return smem_sums && sizeof(T) == 4; }
+
 template <typename T>
 MOE_DEVINL T* at_bytes(void* p, uint32_t at) { return reinterpret_cast<T*>(static_cast<char*>(p) + at); }
 
@@ -382,10 +386,11 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 2 : 1)
     const int step = gridDim.x * groups, t0 = blockIdx.x * groups + g;
     Group grp{g, rank, a.group, dyn + g * kSumFloats};
     const Cols<T, N, KIND> col{rank, a.group, a.D};
+    constexpr bool KEPT = kept_factors<T>(SMEM);
     float* sums = dyn + groups * kSumFloats;            // with SMEM or several groups
     const int sums_floats = SMEM || groups > 1 ? (2 * a.D + 3) / 4 * 4 : 0;
     Ring<T, N, 4, STAGES, KIND, NormGradArgs> in{a, col,
-                                                 reinterpret_cast<char*>(sums + sums_floats + (SMEM ? 0 : 2 * N * a.group)) + g * STAGES * 4 * a.pitch};
+                                                 reinterpret_cast<char*>(sums + sums_floats + (KEPT ? 0 : 2 * N * a.group)) + g * STAGES * 4 * a.pitch};
     const uint32_t skip = step * a.D * (uint32_t)sizeof(T);
     uint32_t at = t0 * a.D * (uint32_t)sizeof(T);
     constexpr int M = SMEM ? 2 : N;
@@ -399,7 +404,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 2 : 1)
     pdl_wait();
 #pragma unroll
     for (int i = 0; i < STAGES; ++i) in.fetch(at + i * skip, t0 + i * step < a.T);
-    Factors<N, SMEM> fac;
+    Factors<N, KEPT> fac;
     fac.at = reinterpret_cast<float4*>(sums + sums_floats);
     fac.rank = rank;
     fac.size = a.group;
@@ -501,27 +506,27 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 2 : 1)
     }
 }
 
-// Column sums of the blocks' partials: 32 columns per block, each of its 32 warps
-// a share of the partials, the shares added in order.
-__global__ void __launch_bounds__(1024) block_norm_join_kernel(const float* __restrict__ part, int n, int D,
+// Column sums of the blocks' partials: 32 columns per block, an eighth of the
+// partials per warp, the eighths added in order.
+__global__ void __launch_bounds__(256) block_norm_join_kernel(const float* __restrict__ part, int n, int D,
                                                               const float* w_post, const float* gate, float* dw_next,
                                                               float* dw_post, float* dgate) {
-    __shared__ float sums[32][32];
+    __shared__ float sums[8][32];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     const bool next = blockIdx.y == 0;
     pdl_wait();
     if (next ? !dw_next : !dw_post && !dgate) return;
-    const int each = (n + 31) / 32, i1 = min(n, (w + 1) * each);
+    const int each = (n + 7) / 8, i1 = min(n, (w + 1) * each);
     float s = 0.f;
     if (c < D) {
-#pragma unroll 10
+#pragma unroll 8
         for (int i = w * each; i < i1; ++i) s += __ldg(part + ((size_t)i * 2 + blockIdx.y) * D + c);
     }
     sums[w][lane] = s;
     __syncthreads();
     if (w > 0 || c >= D) return;
 #pragma unroll
-    for (int i = 1; i < 32; ++i) s += sums[i][lane];
+    for (int i = 1; i < 8; ++i) s += sums[i][lane];
     if (next) {
         dw_next[c] = s;
     } else {
@@ -575,7 +580,7 @@ cudaError_t run_norm_backward(NormGradArgs a, int* blocks, cudaStream_t s) {
     *blocks = n.blocks(a.T, THREADS == kNormThreads ? 2 * sms : sms);
     const size_t sums = SMEM || n.groups > 1 ? (size_t)(2 * a.D + 3) / 4 * 16 : 0;
     return launch_pdl(kernel, dim3(*blocks), dim3(n.group * n.groups),
-                      sums + (SMEM ? 0 : (size_t)n.group * N * 8) + (size_t)n.groups * (kSumFloats * 4 + STAGES * 4 * n.pitch), s, a);
+                      sums + (kept_factors<T>(SMEM) ? 0 : (size_t)n.group * N * 8) + (size_t)n.groups * (kSumFloats * 4 + STAGES * 4 * n.pitch), s, a);
 }
 
 // A thread has 16 bytes of a row (twice that for fp32 rows beyond 4,096).  Blocks
@@ -597,7 +602,7 @@ cudaError_t pick_norm_backward(const NormGradArgs& a, int* blocks, cudaStream_t 
     if (a.D <= kNormThreads * N) return run_norm_backward<T, N, 3, kNormThreads, false, KIND>(a, blocks, s);
     if (a.D <= 512 * N) return run_norm_backward<T, N, 3, 512, false, KIND>(a, blocks, s);
     if constexpr (N == 8) {
-        return run_norm_backward<T, N, 2, 1024, true, KIND>(a, blocks, s);
+        return run_norm_backward<T, N, 1, 1024, true, KIND>(a, blocks, s);
     } else {
         if (a.D <= 1024 * N) return run_norm_backward<T, N, 2, 1024, false, KIND>(a, blocks, s);
         return run_norm_backward<T, 8, 1, 1024, true, KIND>(a, blocks, s);
@@ -705,6 +710,6 @@ extern "C" moe_status moe_block_norm_backward(const void* dx_out, const void* dn
                                  : pick_norm_backward<Tp, ANY>(a, &blocks, s));
     });
     if (st != MOE_OK || (!dw_next && !dw_post && !dgate_cols)) return st;
-    return ops_status(launch_pdl(block_norm_join_kernel, dim3((D + 31) / 32, 2), dim3(1024), 0, s, (const float*)ws, blocks,
+    return ops_status(launch_pdl(block_norm_join_kernel, dim3((D + 31) / 32, 2), dim3(256), 0, s, (const float*)ws, blocks,
                                  D, w_post, per_token ? nullptr : gate, dw_next, dw_post, dgate_cols));
 }
