@@ -24,7 +24,7 @@ namespace cg = cooperative_groups;
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanBlocks = 8;             // one cluster
-constexpr int kPlanHeld = 8;               // rounds of 32 pairs that a warp keeps in registers between its walks
+constexpr int kPlanHeld = 8;               // rounds of 32 pairs that a warp loads together
 constexpr int kSmallPairs = 4096;          // up to here every block makes its part of the plan itself
 constexpr int kSmallThreads = 256;
 constexpr int kNoExpert = 0x7fffffff;
@@ -57,104 +57,132 @@ MOE_DEVINL int block_scan(int v, int* wsum) {
 }
 
 // The plan: a stable counting sort of the P pairs by expert, in one cluster.
-// Warp w of block b owns the pairs of segment (b, w), 32 at a time in order;
-// lanes with the same expert find one another (match), the first of them adds
-// their number to the warp's counter of that expert.  An exclusive scan over
-// (expert, block, warp) turns the counters into first rows, and a second walk
-// over the pairs hands them out.  A chain of memory latencies bounds it, so the
-// ids of up to 8 rounds are loaded together and kept for the second walk.
+// Warp w of block b owns the pairs of segment (b, w), 32 at a time in order.
+// Lanes with the same expert find one another by a ballot for each bit of the
+// expert's number (10 ballots and selects took 400 clocks a round with 32 warps
+// per SM, __match_any_sync 1,960); the first of them adds their number to the
+// warp's counter of that expert and tells the others what it held, so that every
+// pair knows its rank among the warp's pairs of its expert.  An exclusive scan
+// over (expert, block, warp) gives the ranks their first row.  A chain of
+// latencies bounds it, so the ids of 8 rounds are loaded together, and the ranks
+// of the first 8 rounds stay in registers (those of longer segments wait in
+// pair_row): one walk does all the matching.  row_pair null: the next kernel
+// writes it (scattered words, too many for 8 SMs: 3 us of 40,960 pairs).
 __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThreads)
     permute_plan_kernel(const int32_t* __restrict__ ids, int P, int E, const int32_t* __restrict__ slot_table,
                         int n_slots, int32_t* __restrict__ offsets, int32_t* __restrict__ pair_row,
                         int32_t* __restrict__ row_pair) {
     extern __shared__ int32_t count[];          // [warp][E]
     __shared__ int block_total[kOpsMaxE];       // of each expert, read by the cluster's other blocks
+    __shared__ int first[kOpsMaxE];             // first row of the block's pairs of each expert
     __shared__ int wsum[32];
     cg::cluster_group cluster = cg::this_cluster();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, b = (int)cluster.block_rank();
     for (int i = threadIdx.x; i < kPlanWarps * E; i += kPlanThreads) count[i] = 0;
     pdl_wait();
-    __syncthreads();
+    pdl_launch_dependents();
     const int rounds = (P + kPlanBlocks * kPlanThreads - 1) / (kPlanBlocks * kPlanThreads);
     const int p0 = (b * kPlanWarps + w) * rounds * 32 + lane;
     int32_t* mine = count + w * E;
-    int held[kPlanHeld];
-    for (int i0 = 0; i0 < rounds; i0 += kPlanHeld) {
+    int key[kPlanHeld], rank[kPlanHeld];
+    auto load = [&](int i0) {
 #pragma unroll
         for (int i = 0; i < kPlanHeld; ++i) {
             const int p = p0 + (i0 + i) * 32;
-            held[i] = i0 + i < rounds && p < P ? taken_expert(ids, p, E, slot_table, n_slots) : kNoExpert;
+            key[i] = i0 + i < rounds && p < P ? __ldg(ids + p) : -1;
         }
+        if (slot_table) {
+            int slot[kPlanHeld];
+#pragma unroll
+            for (int i = 0; i < kPlanHeld; ++i)
+                slot[i] = (uint32_t)key[i] < (uint32_t)E ? __ldg(slot_table + key[i]) : 0;
+#pragma unroll
+            for (int i = 0; i < kPlanHeld; ++i)
+                if (slot[i] >= 0 && slot[i] < n_slots) key[i] = -1;
+        }
+#pragma unroll
+        for (int i = 0; i < kPlanHeld; ++i)
+            if ((uint32_t)key[i] >= (uint32_t)E) key[i] = E;        // no expert
+    };
+    const int bits = 32 - __clz(E);             // of the numbers 0..E
+    load(0);
+    __syncthreads();
+    for (int i0 = 0; i0 < rounds; i0 += kPlanHeld) {
+        if (i0 > 0) load(i0);
 #pragma unroll
         for (int i = 0; i < kPlanHeld; ++i) {
             if (i0 + i >= rounds) break;
-            const uint32_t peers = __match_any_sync(0xffffffffu, held[i]);
-            if (held[i] != kNoExpert && lane == __ffs(peers) - 1) mine[held[i]] += __popc(peers);
-            __syncwarp();
+            uint32_t peers = 0xffffffffu;
+            for (int j = 0; j < bits; ++j) {
+                const bool one = key[i] >> j & 1;
+                const uint32_t ones = __ballot_sync(0xffffffffu, one);
+                peers &= one ? ones : ~ones;
+            }
+            const int leader = __ffs(peers) - 1;
+            int held = 0;
+            if (lane == leader && key[i] < E) {
+                held = mine[key[i]];
+                mine[key[i]] = held + __popc(peers);
+            }
+            rank[i] = __shfl_sync(0xffffffffu, held, leader) + __popc(peers & ((1u << lane) - 1u));
+            const int p = p0 + (i0 + i) * 32;
+            if (rounds > kPlanHeld && p < P) pair_row[p] = rank[i];
         }
     }
     __syncthreads();
     // thread e: the expert's total in this block, and its warps' counters as offsets inside it
-    int in_block = 0;
     if (threadIdx.x < E) {
-#pragma unroll 8
+        int c[kPlanWarps], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kPlanWarps; ++i) c[i] = count[i * E + threadIdx.x];
+#pragma unroll
         for (int i = 0; i < kPlanWarps; ++i) {
-            const int c = count[i * E + threadIdx.x];
-            count[i * E + threadIdx.x] = in_block;
-            in_block += c;
+            count[i * E + threadIdx.x] = sum;
+            sum += c[i];
         }
-        block_total[threadIdx.x] = in_block;
+        block_total[threadIdx.x] = sum;
     }
     cluster.sync();
     int total = 0, before = 0;
     if (threadIdx.x < E) {
+        int c[kPlanBlocks];
+#pragma unroll
+        for (int i = 0; i < kPlanBlocks; ++i) c[i] = cluster.map_shared_rank(block_total, i)[threadIdx.x];
 #pragma unroll
         for (int i = 0; i < kPlanBlocks; ++i) {
-            const int c = cluster.map_shared_rank(block_total, i)[threadIdx.x];
-            total += c;
-            if (i < b) before += c;
+            total += c[i];
+            if (i < b) before += c[i];
         }
     }
     const int base = block_scan(total, wsum) - total;
     if (threadIdx.x < E) {
+        first[threadIdx.x] = base + before;
         if (b == 0) {
             offsets[threadIdx.x] = base;
             if (threadIdx.x == E - 1) offsets[E] = base + total;
         }
-#pragma unroll 8
-        for (int i = 0; i < kPlanWarps; ++i) count[i * E + threadIdx.x] += base + before;
     }
-    cluster.sync();                             // no block leaves while another reads its totals
+    cluster.sync();                             // `first` is there, and no block leaves while another reads its totals
     for (int i0 = 0; i0 < rounds; i0 += kPlanHeld) {
-        if (rounds > kPlanHeld) {
-#pragma unroll
-            for (int i = 0; i < kPlanHeld; ++i) {
-                const int p = p0 + (i0 + i) * 32;
-                held[i] = i0 + i < rounds && p < P ? taken_expert(ids, p, E, slot_table, n_slots) : kNoExpert;
-            }
-        }
+        if (rounds > kPlanHeld) load(i0);
 #pragma unroll
         for (int i = 0; i < kPlanHeld; ++i) {
             const int p = p0 + (i0 + i) * 32;
-            if (i0 + i >= rounds) break;
-            const uint32_t peers = __match_any_sync(0xffffffffu, held[i]);
+            if (i0 + i >= rounds || p >= P) break;
             int row = -1;
-            if (held[i] != kNoExpert) row = mine[held[i]] + __popc(peers & ((1u << lane) - 1u));
-            __syncwarp();
-            if (held[i] != kNoExpert && lane == __ffs(peers) - 1) mine[held[i]] += __popc(peers);
-            __syncwarp();
-            if (p < P) {
-                pair_row[p] = row;
-                if (row >= 0) row_pair[row] = p;
+            if (key[i] < E) {
+                row = first[key[i]] + mine[key[i]] + (rounds > kPlanHeld ? pair_row[p] : rank[i]);
+                if (row_pair) row_pair[row] = p;
             }
+            pair_row[p] = row;
         }
     }
 }
 
-// x[t] into the rows row[0..k): the token is read once.
+// x[t] into the rows row[0..k), from column `c` on: the token is read once.
 template <typename T, int V>
-MOE_DEVINL void scatter_token(const T* x, int t, const int32_t* row, int k, int D, T* rows) {
-    for (int c = threadIdx.x * V; c < D; c += blockDim.x * V) {
+MOE_DEVINL void scatter_token(const T* x, int t, const int32_t* row, int k, int D, T* rows, int c) {
+    for (; c < D; c += blockDim.x * V) {
         const Pack<T, V> a = load_pack<T, V>(x + (size_t)t * D + c);
         for (int r = 0; r < k; ++r)
             if (row[r] >= 0) store_pack<T, V>(rows + (size_t)row[r] * D + c, a);
@@ -223,19 +251,31 @@ __global__ void __launch_bounds__(kSmallThreads) permute_small_kernel(
     }
     if (!x) return;
     __syncthreads();
-    scatter_token<T, V>(x, t, row, k, D, rows);
+    scatter_token<T, V>(x, t, row, k, D, rows, threadIdx.x * V);
 }
 
+// The copies behind the plan, and row_pair.  The first columns of x are read while the plan is
+// still made: its blocks let this kernel start once they have waited for the
+// kernels that may have written x.
 template <typename T, int V>
 __global__ void __launch_bounds__(512) permute_rows_kernel(const T* __restrict__ x,
                                                            const int32_t* __restrict__ pair_row, int k, int D,
-                                                           T* __restrict__ rows) {
+                                                           T* __restrict__ rows, int32_t* __restrict__ row_pair) {
     __shared__ int32_t row[kMaxTopK];
+    const int t = blockIdx.x, c = threadIdx.x * V;
+    Pack<T, V> a;
+    if (c < D) a = load_pack<T, V>(x + (size_t)t * D + c);
     pdl_wait();
-    const int t = blockIdx.x;
-    if (threadIdx.x < k) row[threadIdx.x] = __ldg(pair_row + t * k + threadIdx.x);
+    if (threadIdx.x < k) {
+        const int p = t * k + threadIdx.x, i = __ldg(pair_row + p);
+        row[threadIdx.x] = i;
+        if (i >= 0) row_pair[i] = p;
+    }
     __syncthreads();
-    scatter_token<T, V>(x, t, row, k, D, rows);
+    if (c < D)
+        for (int r = 0; r < k; ++r)
+            if (row[r] >= 0) store_pack<T, V>(rows + (size_t)row[r] * D + c, a);
+    scatter_token<T, V>(x, t, row, k, D, rows, c + blockDim.x * V);
 }
 
 // out[t] = sum_r w[t,r] rows[row(t,r)], r ascending in fp32 (w NULL: 1).  A
@@ -404,11 +444,11 @@ moe_status launch_permute(const int32_t* ids, int T_, int k, int E, const int32_
         return MOE_ERR_CUDA;
     const cudaError_t e = launch_pdl(permute_plan_kernel, dim3(kPlanBlocks), dim3(kPlanThreads),
                                      (size_t)kPlanWarps * E * 4, s, ids, P, E, slot_table, n_slots, offsets, pair_row,
-                                     row_pair);
+                                     x ? nullptr : row_pair);
     if (e != cudaSuccess || !x) return ops_status(e);
     auto kernel = wide ? permute_rows_kernel<T, V> : permute_rows_kernel<T, 1>;
     return ops_status(launch_pdl(kernel, dim3(T_), dim3(row_threads(wide ? D / V : D)), 0, s, x,
-                                 (const int32_t*)pair_row, k, D, rows));
+                                 (const int32_t*)pair_row, k, D, rows, row_pair));
 }
 
 bool out_dtype_ok(int dtype, int out_dtype) { return out_dtype == dtype || out_dtype == MOE_F32; }
