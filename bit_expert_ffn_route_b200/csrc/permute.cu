@@ -21,9 +21,9 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 512;          // two experts per thread
 constexpr int kPlanWarps = kPlanThreads / 32;
-constexpr int kPlanBlocks = 8;             // one cluster
+constexpr int kPlanBlocks = 16;            // one cluster (of the size that a kernel has to ask for)
 constexpr int kPlanHeld = 8;               // rounds of 32 pairs that a warp loads together
 constexpr int kSmallPairs = 4096;          // up to here every block makes its part of the plan itself
 constexpr int kSmallThreads = 256;
@@ -59,8 +59,8 @@ MOE_DEVINL int block_scan(int v, int* wsum) {
 // The plan: a stable counting sort of the P pairs by expert, in one cluster.
 // Warp w of block b owns the pairs of segment (b, w), 32 at a time in order.
 // Lanes with the same expert find one another by a ballot for each bit of the
-// expert's number (10 ballots and selects took 400 clocks a round with 32 warps
-// per SM, __match_any_sync 1,960); the first of them adds their number to the
+// expert's number (a round of 8 warps per scheduler takes 1,400 clocks so,
+// 1,960 with __match_any_sync); the first of them adds their number to the
 // warp's counter of that expert and tells the others what it held, so that every
 // pair knows its rank among the warp's pairs of its expert.  An exclusive scan
 // over (expert, block, warp) gives the ranks their first row.  A chain of
@@ -72,18 +72,19 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
     permute_plan_kernel(const int32_t* __restrict__ ids, int P, int E, const int32_t* __restrict__ slot_table,
                         int n_slots, int32_t* __restrict__ offsets, int32_t* __restrict__ pair_row,
                         int32_t* __restrict__ row_pair) {
-    extern __shared__ int32_t count[];          // [warp][E]
-    __shared__ int block_total[kOpsMaxE];       // of each expert, read by the cluster's other blocks
-    __shared__ int first[kOpsMaxE];             // first row of the block's pairs of each expert
+    extern __shared__ __align__(8) int32_t count[];     // [warp][Ep]
+    __shared__ __align__(8) int block_total[kOpsMaxE];       // of each expert, read by the cluster's other blocks
+    __shared__ __align__(8) int first[kOpsMaxE];           // first row of the block's pairs of each expert
     __shared__ int wsum[32];
     cg::cluster_group cluster = cg::this_cluster();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, b = (int)cluster.block_rank();
-    for (int i = threadIdx.x; i < kPlanWarps * E; i += kPlanThreads) count[i] = 0;
+    const int Ep = (E + 1) & ~1, e0 = 2 * threadIdx.x;  // this thread's experts: e0, e0 + 1
+    for (int i = threadIdx.x; i < kPlanWarps * Ep / 2; i += kPlanThreads) reinterpret_cast<int2*>(count)[i] = {0, 0};
     pdl_wait();
     pdl_launch_dependents();
     const int rounds = (P + kPlanBlocks * kPlanThreads - 1) / (kPlanBlocks * kPlanThreads);
     const int p0 = (b * kPlanWarps + w) * rounds * 32 + lane;
-    int32_t* mine = count + w * E;
+    int32_t* mine = count + w * Ep;
     int key[kPlanHeld], rank[kPlanHeld];
     auto load = [&](int i0) {
 #pragma unroll
@@ -104,7 +105,6 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
         for (int i = 0; i < kPlanHeld; ++i)
             if ((uint32_t)key[i] >= (uint32_t)E) key[i] = E;        // no expert
     };
-    const int bits = 32 - __clz(E);             // of the numbers 0..E
     load(0);
     __syncthreads();
     for (int i0 = 0; i0 < rounds; i0 += kPlanHeld) {
@@ -113,10 +113,11 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
         for (int i = 0; i < kPlanHeld; ++i) {
             if (i0 + i >= rounds) break;
             uint32_t peers = 0xffffffffu;
-            for (int j = 0; j < bits; ++j) {
-                const bool one = key[i] >> j & 1;
-                const uint32_t ones = __ballot_sync(0xffffffffu, one);
-                peers &= one ? ones : ~ones;
+#pragma unroll
+            for (int j = 0; j < 11; ++j) {              // of the numbers 0..E, E <= 1024
+                if (E >> j == 0) break;
+                const bool one = key[i] & (1 << j);
+                peers &= __ballot_sync(0xffffffffu, one) ^ (one ? 0u : 0xffffffffu);
             }
             const int leader = __ffs(peers) - 1;
             int held = 0;
@@ -130,36 +131,38 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
         }
     }
     __syncthreads();
-    // thread e: the expert's total in this block, and its warps' counters as offsets inside it
-    if (threadIdx.x < E) {
-        int c[kPlanWarps], sum = 0;
+    // the experts' totals in this block, and their warps' counters as offsets inside it
+    if (e0 < E) {
+        int2 c[kPlanWarps], sum = {0, 0};
 #pragma unroll
-        for (int i = 0; i < kPlanWarps; ++i) c[i] = count[i * E + threadIdx.x];
+        for (int i = 0; i < kPlanWarps; ++i) c[i] = *reinterpret_cast<const int2*>(count + i * Ep + e0);
 #pragma unroll
         for (int i = 0; i < kPlanWarps; ++i) {
-            count[i * E + threadIdx.x] = sum;
-            sum += c[i];
+            *reinterpret_cast<int2*>(count + i * Ep + e0) = sum;
+            sum.x += c[i].x, sum.y += c[i].y;
         }
-        block_total[threadIdx.x] = sum;
+        *reinterpret_cast<int2*>(block_total + e0) = sum;
     }
     cluster.sync();
-    int total = 0, before = 0;
-    if (threadIdx.x < E) {
-        int c[kPlanBlocks];
+    int2 total = {0, 0}, before = {0, 0};
+    if (e0 < E) {
+        int2 c[kPlanBlocks];
 #pragma unroll
-        for (int i = 0; i < kPlanBlocks; ++i) c[i] = cluster.map_shared_rank(block_total, i)[threadIdx.x];
+        for (int i = 0; i < kPlanBlocks; ++i)
+            c[i] = *reinterpret_cast<const int2*>(cluster.map_shared_rank(block_total, i) + e0);
 #pragma unroll
         for (int i = 0; i < kPlanBlocks; ++i) {
-            total += c[i];
-            if (i < b) before += c[i];
+            total.x += c[i].x, total.y += c[i].y;
+            if (i < b) before.x += c[i].x, before.y += c[i].y;
         }
     }
-    const int base = block_scan(total, wsum) - total;
-    if (threadIdx.x < E) {
-        first[threadIdx.x] = base + before;
+    const int base = block_scan(total.x + total.y, wsum) - total.x - total.y;
+    if (e0 < E) {
+        *reinterpret_cast<int2*>(first + e0) = {base + before.x, base + total.x + before.y};
         if (b == 0) {
-            offsets[threadIdx.x] = base;
-            if (threadIdx.x == E - 1) offsets[E] = base + total;
+            offsets[e0] = base;
+            offsets[e0 + 1] = base + total.x;           // offsets[E], if e0 is the last expert
+            if (e0 + 2 == E) offsets[E] = base + total.x + total.y;
         }
     }
     cluster.sync();                             // `first` is there, and no block leaves while another reads its totals
@@ -439,11 +442,13 @@ moe_status launch_permute(const int32_t* ids, int T_, int k, int E, const int32_
     static std::atomic<uint64_t> set{0};
     if (!once_per_device(set, [] {
             return cudaFuncSetAttribute(permute_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        kPlanWarps * kOpsMaxE * 4) == cudaSuccess;
+                                        kPlanWarps * kOpsMaxE * 4) == cudaSuccess &&
+                   cudaFuncSetAttribute(permute_plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+                       cudaSuccess;
         }))
         return MOE_ERR_CUDA;
     const cudaError_t e = launch_pdl(permute_plan_kernel, dim3(kPlanBlocks), dim3(kPlanThreads),
-                                     (size_t)kPlanWarps * E * 4, s, ids, P, E, slot_table, n_slots, offsets, pair_row,
+                                     (size_t)kPlanWarps * ((E + 1) / 2 * 2) * 4, s, ids, P, E, slot_table, n_slots, offsets, pair_row,
                                      x ? nullptr : row_pair);
     if (e != cudaSuccess || !x) return ops_status(e);
     auto kernel = wide ? permute_rows_kernel<T, V> : permute_rows_kernel<T, 1>;
