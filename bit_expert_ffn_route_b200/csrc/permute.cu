@@ -12,6 +12,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "once.cuh"
 #include "rows.cuh"
 #include "sync.cuh"
@@ -28,6 +30,9 @@ constexpr int kPlanHeld = 8;               // rounds of 32 pairs that a warp loa
 constexpr int kSmallPairs = 4096;          // up to here every block makes its part of the plan itself
 constexpr int kSmallThreads = 256;
 constexpr int kNoExpert = 0x7fffffff;
+constexpr int kSumThreads = 128;           // of an unpermute block
+constexpr int kDotThreads = 256;           // of a block of its gradient
+constexpr int kManyPairs = 2048;           // from here on a warp per pair fills the GPU
 
 // The expert of pair p, or kNoExpert if the pair is not taken.
 MOE_DEVINL int taken_expert(const int32_t* ids, int p, int E, const int32_t* slot_table, int n_slots) {
@@ -281,102 +286,148 @@ __global__ void __launch_bounds__(512) permute_rows_kernel(const T* __restrict__
     scatter_token<T, V>(x, t, row, k, D, rows, c + blockDim.x * V);
 }
 
-// out[t] = sum_r w[t,r] rows[row(t,r)], r ascending in fp32 (w NULL: 1).  A
-// thread owns U packs of the token, blockDim apart, and loads them from up to R
-// rows before it adds the first.
-template <typename T, typename TO, int V, int U, int R>
-__global__ void __launch_bounds__(128) unpermute_kernel(const T* __restrict__ rows, int n_rows,
-                                                        const int32_t* __restrict__ pair_row,
-                                                        const float* __restrict__ weights, int k, int D,
-                                                        TO* __restrict__ out) {
+// out[t] = sum_r w[t,r] rows[row(t,r)], r ascending in fp32 (w NULL: 1).  `each`
+// threads (a power of two) take a token, each of them U packs of it, `each` packs
+// apart, and load them from all of the token's up to R rows before they add the
+// first; short rows put several tokens in a block.  EACH: `each` as a constant
+// where U > 1, so that a thread's packs differ by constant offsets (with `each` in
+// a register 20,011 x 3 x 1,001 fp32 took 72 us instead of 58).
+template <typename T, typename TO, int V, int U, int R, int EACH>
+__global__ void __launch_bounds__(kSumThreads) unpermute_kernel(const T* __restrict__ rows, int n_rows,
+                                                                const int32_t* __restrict__ pair_row,
+                                                                const float* __restrict__ weights, int T_, int k, int D,
+                                                                int each_, TO* __restrict__ out) {
+    const int each = EACH ? EACH : each_;
+    __shared__ int s_row[kSumThreads / 8 * kMaxTopK];
+    __shared__ float s_w[kSumThreads / 8 * kMaxTopK];
     pdl_wait();
-    const int t = blockIdx.x;
-    const int c0 = (blockIdx.y * U * 128 + threadIdx.x) * V;
-    float acc[U][V];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc[u][i] = 0.f;
-    int row[R];
-    float w[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        row[r] = r < k ? __ldg(pair_row + t * k + r) : -1;
-        w[r] = r < k && weights ? __ldg(weights + t * k + r) : 1.f;
+    const int tokens = kSumThreads / each, t0 = blockIdx.x * tokens, mine = threadIdx.x / each;
+    for (int i = threadIdx.x; i < tokens * k; i += kSumThreads) {
+        const int p = t0 * k + i;
+        int row = -1;
+        if (p < T_ * k) {
+            row = __ldg(pair_row + p);
+            s_w[i] = weights ? __ldg(weights + p) : 1.f;
+        }
+        s_row[i] = row < n_rows ? row : -1;
     }
+    __syncthreads();
+    const int t = t0 + mine, c0 = (blockIdx.y * U * each + threadIdx.x % each) * V;
+    if (t >= T_) return;
+    int row[R];
     Pack<T, V> y[U][R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        if (row[r] >= n_rows) row[r] = -1;
+        row[r] = r < k ? s_row[mine * k + r] : -1;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int c = c0 + u * 128 * V;
+            const int c = c0 + u * each * V;
             if (row[r] >= 0 && c < D) y[u][r] = load_pack<T, V>(rows + (size_t)row[r] * D + c);
         }
     }
 #pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int u = 0; u < U; ++u) hold(y[u][r]);
+#pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int c = c0 + u * 128 * V;
+        const int c = c0 + u * each * V;
         if (c >= D) continue;
+        float acc[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = 0.f;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             if (row[r] < 0) continue;
+            const float w = s_w[mine * k + r];
             float v[V];
             unpack<T, V>(y[u][r], v);
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[u][i] = __fmaf_rn(w[r], v[i], acc[u][i]);
+            for (int i = 0; i < V; ++i) acc[i] = __fmaf_rn(w, v[i], acc[i]);
         }
-        store_f32<TO, V>(out + (size_t)t * D + c, acc[u]);
+        store_f32<TO, V>(out + (size_t)t * D + c, acc);
     }
 }
 
-// drows[row(p)] = w[p] dout[t] and dw[p] = <dout[t], rows[row(p)]>: a warp per
-// pair, U packs in flight per lane.  The k warps of a token read dout[t] after
+// drows[row(p)] = w[p] dout[t] and dw[p] = <dout[t], rows[row(p)]>: EACH threads
+// per pair, U packs in flight per thread.  The pairs of a token read dout[t] after
 // one another, so all but the first find it in the caches.
-template <typename T, typename TO, int V, int U>
-__global__ void __launch_bounds__(256) unpermute_backward_kernel(const TO* __restrict__ dout,
-                                                                 const T* __restrict__ rows, int n_rows,
-                                                                 const int32_t* __restrict__ pair_row,
-                                                                 const float* __restrict__ weights, int P, int k, int D,
-                                                                 T* __restrict__ drows, float* __restrict__ dweights) {
+template <typename T, typename TO, int V, int U, int EACH>
+__global__ void __launch_bounds__(kDotThreads) unpermute_backward_kernel(const TO* __restrict__ dout,
+                                                                         const T* __restrict__ rows, int n_rows,
+                                                                         const int32_t* __restrict__ pair_row,
+                                                                         const float* __restrict__ weights, int P, int k,
+                                                                         int D, T* __restrict__ drows,
+                                                                         float* __restrict__ dweights) {
+    constexpr int each = EACH;
+    __shared__ float part[kDotThreads / 32];
     pdl_wait();
-    const int p = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (p >= P) return;
-    const int row = __ldg(pair_row + p);
-    const bool held = row >= 0 && row < n_rows;
+    const int p = blockIdx.x * (kDotThreads / each) + threadIdx.x / each, rank = threadIdx.x % each;
+    const int row = p < P ? __ldg(pair_row + p) : -1;
     float dot = 0.f;
-    if (held) {
+    if (row >= 0 && row < n_rows) {
         const float w = weights ? __ldg(weights + p) : 1.f;
         const TO* d = dout + (size_t)(p / k) * D;
         const size_t at = (size_t)row * D;
-        for (int c0 = lane * V; c0 < D; c0 += U * 32 * V) {
+        for (int c0 = rank * V; c0 < D; c0 += U * each * V) {
+            constexpr int H = V * (int)sizeof(TO) > 16 ? 2 : 1, W = V / H;      // dout's accesses per pack
             Pack<T, V> y[U];
-            float g[U][V];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (c0 + u * 32 * V < D && dweights) y[u] = load_pack<T, V>(rows + at + c0 + u * 32 * V);
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (c0 + u * 32 * V < D) load_f32<TO, V>(d + c0 + u * 32 * V, g[u]);
+            Pack<TO, W> e[U][H];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (c0 + u * 32 * V >= D) continue;
+                const int c = c0 + u * each * V;
+                if (c < D && dweights) y[u] = load_pack<T, V>(rows + at + c);
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+                    if (c < D) e[u][h] = load_pack<TO, W>(d + c + h * W);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                hold(y[u]);
+#pragma unroll
+                for (int h = 0; h < H; ++h) hold(e[u][h]);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (c0 + u * each * V >= D) continue;
+                float g[V];
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    float v[W];
+                    unpack<TO, W>(e[u][h], v);
+#pragma unroll
+                    for (int i = 0; i < W; ++i) g[h * W + i] = v[i];
+                }
                 if (dweights) {
                     float v[V];
                     unpack<T, V>(y[u], v);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) dot = __fmaf_rn(g[u][i], v[i], dot);
+                    for (int i = 0; i < V; ++i) dot = __fmaf_rn(g[i], v[i], dot);
                 }
                 if (drows) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) g[u][i] *= w;
-                    store_f32<T, V>(drows + at + c0 + u * 32 * V, g[u]);
+                    for (int i = 0; i < V; ++i) g[i] *= w;
+                    store_f32<T, V>(drows + at + c0 + u * each * V, g);
                 }
             }
         }
-        dot = warp_sum(dot);
     }
-    if (dweights && lane == 0) dweights[p] = dot;
+    if (!dweights) return;
+#pragma unroll
+    for (int o = (each < 32 ? each : 32) / 2; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if constexpr (each > 32) {
+        if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = dot;
+        __syncthreads();
+        if (rank == 0)
+            for (int i = 1; i < each / 32; ++i) dot += part[threadIdx.x / 32 + i];
+    }
+    if (rank == 0 && p < P) dweights[p] = dot;
+}
+
+// The least power of two >= n, in [lo, hi].
+inline int threads_for(int n, int lo, int hi) {
+    while (lo < n && lo < hi) lo *= 2;
+    return lo;
 }
 
 // Threads for a row of n packs: whole warps, at most 512, the row's passes equally full.
@@ -394,23 +445,41 @@ inline bool wide_rows(int D, size_t elem, P... p) {
 template <typename T, typename TO, int V, int U>
 cudaError_t run_unpermute(const void* rows, int n_rows, const int32_t* pair_row, const float* weights, int T_, int k,
                           int D, void* out, cudaStream_t s) {
-    const dim3 grid(T_, (D + U * 128 * V - 1) / (U * 128 * V));
+    const int packs = (D + V - 1) / V, need = (packs + U - 1) / U;
+    const int each = U == 1 ? threads_for(need, 8, kSumThreads) : need <= 8 ? 8 : need <= 32 ? 32 : kSumThreads;
+    const dim3 grid((T_ + kSumThreads / each - 1) / (kSumThreads / each), (packs + U * each - 1) / (U * each));
     auto go = [&](auto kernel) {
-        return launch_pdl(kernel, grid, dim3(128), 0, s, static_cast<const T*>(rows), n_rows, pair_row, weights, k, D,
-                          static_cast<TO*>(out));
+        return launch_pdl(kernel, grid, dim3(kSumThreads), 0, s, static_cast<const T*>(rows), n_rows, pair_row, weights,
+                          T_, k, D, each, static_cast<TO*>(out));
     };
-    if (k <= 4) return go(unpermute_kernel<T, TO, V, U, 4>);
-    if (k <= 8) return go(unpermute_kernel<T, TO, V, U, 8>);
-    if (k <= 12) return go(unpermute_kernel<T, TO, V, U, 12>);
-    return go(unpermute_kernel<T, TO, V, U, 16>);
+    auto by_rank = [&](auto e) {
+        constexpr int EACH = decltype(e)::value;
+        if (k <= 4) return go(unpermute_kernel<T, TO, V, U, 4, EACH>);
+        if (k <= 8) return go(unpermute_kernel<T, TO, V, U, 8, EACH>);
+        if (k <= 12) return go(unpermute_kernel<T, TO, V, U, 12, EACH>);
+        return go(unpermute_kernel<T, TO, V, U, 16, EACH>);
+    };
+    if constexpr (U == 1) return by_rank(std::integral_constant<int, 0>{});
+    else if (each == 8) return by_rank(std::integral_constant<int, 8>{});
+    else if (each == 32) return by_rank(std::integral_constant<int, 32>{});
+    else return by_rank(std::integral_constant<int, kSumThreads>{});
 }
 template <typename T, typename TO, int V, int U>
 cudaError_t run_unpermute_backward(const void* dout, const void* rows, int n_rows, const int32_t* pair_row,
                                    const float* weights, int P, int k, int D, void* drows, float* dweights,
                                    cudaStream_t s) {
-    return launch_pdl(unpermute_backward_kernel<T, TO, V, U>, dim3((P + 7) / 8), dim3(256), 0, s,
-                      static_cast<const TO*>(dout), static_cast<const T*>(rows), n_rows, pair_row, weights, P, k, D,
-                      static_cast<T*>(drows), dweights);
+    const int need = (D + V * U - 1) / (V * U);
+    auto go = [&](auto e) {
+        constexpr int EACH = decltype(e)::value;
+        return launch_pdl(unpermute_backward_kernel<T, TO, V, U, EACH>,
+                          dim3((P + kDotThreads / EACH - 1) / (kDotThreads / EACH)), dim3(kDotThreads), 0, s,
+                          static_cast<const TO*>(dout), static_cast<const T*>(rows), n_rows, pair_row, weights, P, k, D,
+                          static_cast<T*>(drows), dweights);
+    };
+    if (need <= 8) return go(std::integral_constant<int, 8>{});
+    if (need <= 32 || (V > 1 && P >= kManyPairs)) return go(std::integral_constant<int, 32>{});
+    if (need <= 160) return go(std::integral_constant<int, 128>{});
+    return go(std::integral_constant<int, 256>{});
 }
 
 moe_status launch_unpermute(const void* rows, int n_rows, const int32_t* pair_row, const float* weights, int T_, int k,
@@ -526,11 +595,11 @@ extern "C" moe_status moe_unpermute_backward(const void* dout, int out_dtype, co
         if (out_dtype == MOE_F32)
             return ops_status(wide ? run_unpermute_backward<Tp, float, V, 4>(dout, rows, n_rows, pair_row, weights, P, k,
                                                                              D, drows, dweights, s)
-                                   : run_unpermute_backward<Tp, float, 1, 16>(dout, rows, n_rows, pair_row, weights, P,
+                                   : run_unpermute_backward<Tp, float, 1, 8>(dout, rows, n_rows, pair_row, weights, P,
                                                                               k, D, drows, dweights, s));
         return ops_status(wide ? run_unpermute_backward<Tp, Tp, V, 4>(dout, rows, n_rows, pair_row, weights, P, k, D,
                                                                       drows, dweights, s)
-                               : run_unpermute_backward<Tp, Tp, 1, 16>(dout, rows, n_rows, pair_row, weights, P, k, D,
+                               : run_unpermute_backward<Tp, Tp, 1, 8>(dout, rows, n_rows, pair_row, weights, P, k, D,
                                                                        drows, dweights, s));
     });
 }

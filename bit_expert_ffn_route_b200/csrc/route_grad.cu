@@ -21,8 +21,9 @@ using B16 = __nv_bfloat16;
 constexpr int kSliceThreads = 1024;
 constexpr int kSliceTile = 64;             // tokens whose pairs a slice block holds at a time, times k <= 16: a pair per thread
 constexpr int kSliceMaxE = 800;            // experts whose 128 columns fit in shared memory beside the pairs; 64 beyond
-constexpr int kDwThreads = 128;            // columns of dWr per block: 8 per thread
-constexpr int kDwChunks = 320;            // chunks of pairs that the dWr sums are cut into, about
+constexpr int kDwThreads = 128;            // most threads of a dWr block: 8 columns each
+constexpr int kDwMaxChunk = 3328;          // rows whose places fit in 40 KB of shared memory
+constexpr int kDwSums = 320 * 3072;        // partial sums that the dWr chunks make, about
 constexpr int kDwDepth = 4;                // rows of x in flight per thread
 constexpr int kJoinThreads = 256;
 constexpr int kJoinParts = 4;              // shares of an expert's partial sums, added up at the same time
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(kDwThreads) route_dw_kernel(const float* __res
     pdl_wait();
     const int j0 = blockIdx.x * chunk;
     const int n = min(chunk, min(P, __ldg(offsets + E)) - j0);
-    for (int j = threadIdx.x; j < min(chunk, P - j0); j += kDwThreads) {
+    for (int j = threadIdx.x; j < min(chunk, P - j0); j += blockDim.x) {
         const int p = __ldg(row_pair + j0 + j);     // anything beyond the plan's rows
         int e = -1;
         float dl = 0.f;
@@ -237,10 +238,10 @@ __global__ void __launch_bounds__(kDwThreads) route_dw_kernel(const float* __res
     }
     if (n <= 0) return;
     __syncthreads();
-    for (int j = threadIdx.x; j < n; j += kDwThreads)
+    for (int j = threadIdx.x; j < n; j += blockDim.x)
         if (j > 0 && s_exp[j] != s_exp[j - 1]) s_row[j].x |= 1u;
     __syncthreads();
-    const int c = (blockIdx.y * kDwThreads + threadIdx.x) * 8;
+    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * 8;
     if (c >= D) return;
     Sum8 sum;
     auto flush = [&](int e) {
@@ -336,10 +337,11 @@ __global__ void __launch_bounds__(kJoinThreads) route_join_kernel(const float* _
     }
 }
 
-// Rows per chunk: a multiple of 16.
-int dw_chunk(int P) {
-    const int n = (P + kDwChunks - 1) / kDwChunks;
-    return (n + 15) / 16 * 16;
+// Rows per chunk, a multiple of 16: about kDwSums / D chunks, so that the columns'
+// threads of all chunks are as many whatever D is.
+int dw_chunk(int P, int D) {
+    const int chunks = kDwSums / D, n = (P + chunks - 1) / chunks;
+    return n > kDwMaxChunk ? kDwMaxChunk : (n + 15) / 16 * 16;
 }
 
 moe_status route_grad_shapes(int T, int D, int E, int k) {
@@ -351,7 +353,7 @@ moe_status route_grad_shapes(int T, int D, int E, int k) {
 }
 
 size_t route_grad_ws_bytes(int T, int D, int k) {
-    const int P = T * k, chunk = P ? dw_chunk(P) : 16;
+    const int P = T * k, chunk = P ? dw_chunk(P, D) : 16;
     return 256 + (size_t)2 * ((P + chunk - 1) / chunk) * D * 4;
 }
 
@@ -445,12 +447,12 @@ extern "C" moe_status moe_route_backward(const float* dgates, const float* gates
     cudaError_t e = launch_dx(dgates, gates, ids, Wb, T, D, E, k, reinterpret_cast<const B16*>(dx_add), dlogits,
                               reinterpret_cast<B16*>(dx), s);
     if (e != cudaSuccess || (!dWr && !dbias)) return ops_status(e);
-    const int P = T * k, chunk = dw_chunk(P);
+    const int P = T * k, chunk = dw_chunk(P, D);
     float* part = static_cast<float*>(ws);
     if (dWr)
         e = launch_pdl(route_dw_kernel, dim3((P + chunk - 1) / chunk, (D + kDwThreads * 8 - 1) / (kDwThreads * 8)),
-                       dim3(kDwThreads), (size_t)chunk * (sizeof(uint2) + sizeof(int)), s, (const float*)dlogits, ids, xb, offsets, row_pair, P, D, E, k, chunk, dWr,
-                       part);
+                       dim3(D / 8 < kDwThreads ? D / 8 : kDwThreads), (size_t)chunk * (sizeof(uint2) + sizeof(int)), s,
+                       (const float*)dlogits, ids, xb, offsets, row_pair, P, D, E, k, chunk, dWr, part);
     if (e != cudaSuccess) return ops_status(e);
     return ops_status(launch_pdl(route_join_kernel, dim3(E, (dWr ? (D + kJoinCols - 1) / kJoinCols : 0) + 1), dim3(kJoinThreads), 0, s,
                                  (const float*)dlogits, offsets, row_pair, P, D, chunk, (const float*)part, dWr,

@@ -27,18 +27,30 @@ template <> MOE_DEVINL __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return _
 // V elements moved by one access: 16 bytes, or one element (V = 1).  Packs of
 // 16-bit elements stay packed in 32-bit words until they are used.
 template <int BYTES> struct RawOf { using type = uint32_t; };
-template <> struct RawOf<2> { using type = uint16_t; };
 template <> struct RawOf<8> { using type = uint2; };
 template <> struct RawOf<16> { using type = uint4; };
 template <typename T, int V> using Pack = typename RawOf<V * (int)sizeof(T)>::type;
 
 template <typename T, int V>
 MOE_DEVINL Pack<T, V> load_pack(const T* p) {
-    return *reinterpret_cast<const Pack<T, V>*>(p);
+    if constexpr (V * sizeof(T) == 2) return *reinterpret_cast<const uint16_t*>(p);
+    else return *reinterpret_cast<const Pack<T, V>*>(p);
 }
 template <typename T, int V>
 MOE_DEVINL void store_pack(T* p, const Pack<T, V>& a) {
-    *reinterpret_cast<Pack<T, V>*>(p) = a;
+    if constexpr (V * sizeof(T) == 2) *reinterpret_cast<uint16_t*>(p) = (uint16_t)a;
+    else *reinterpret_cast<Pack<T, V>*>(p) = a;
+}
+
+// Between loads under a condition and their use under the same one: without it the
+// compiler moves the conversion to fp32 into the load's branch, and each load is
+// waited for before the next is issued (unpermute of 4,096 x 10 rows of 3,071
+// bf16: 184 us against 63 us).
+template <typename P>
+MOE_DEVINL void hold(P& a) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&a);
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(P) / 4; ++i) asm volatile("" : "+r"(w[i]));
 }
 
 MOE_DEVINL void unpack_word(float, uint32_t w, float* f) { f[0] = __uint_as_float(w); }
