@@ -30,6 +30,7 @@ constexpr int kPlanHeld = 8;               // rounds of 32 pairs that a warp loa
 constexpr int kSmallPairs = 4096;          // up to here every block makes its part of the plan itself
 constexpr int kSmallThreads = 256;
 constexpr int kNoExpert = 0x7fffffff;
+constexpr int kShiftBytes = 256;           // rows that start anywhere: moved in shifted blocks from this length on
 constexpr int kSumThreads = 128;           // of an unpermute block
 constexpr int kDotThreads = 256;           // of a block of its gradient
 constexpr int kManyPairs = 2048;           // from here on a warp per pair fills the GPU
@@ -286,6 +287,89 @@ __global__ void __launch_bounds__(512) permute_rows_kernel(const T* __restrict__
     scatter_token<T, V>(x, t, row, k, D, rows, c + blockDim.x * V);
 }
 
+// Rows that start anywhere.  A matrix row's bytes from its first 16-byte boundary
+// on are `body` blocks of 16; `head` bytes come before and `tail` bytes after them.
+struct Row16 {
+    int head, body, tail;
+    MOE_DEVINL Row16(const void* row, int bytes) {
+        head = (16 - (int)((uintptr_t)row & 15)) & 15;
+        body = (bytes - head) / 16;
+        tail = bytes - head - 16 * body;
+    }
+};
+
+// 16 bytes from byte `at` (any) of a buffer in shared memory; at % 16 is the same
+// in all lanes.
+MOE_DEVINL uint4 bytes16(const uint4* buf, int at) {
+    const uint4 a = buf[at / 16];
+    if (at % 16 == 0) return a;
+    const uint4 b = buf[at / 16 + 1];
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const int bits = at % 4 * 8;
+    uint4 r;
+    switch (at % 16 / 4) {
+        case 0: r = {w[0], w[1], w[2], w[3]}; if (bits) r = {__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits)}; break;
+        case 1: r = {__funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits), __funnelshift_r(w[4], w[5], bits)}; break;
+        case 2: r = {__funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits), __funnelshift_r(w[4], w[5], bits), __funnelshift_r(w[5], w[6], bits)}; break;
+        default: r = {__funnelshift_r(w[3], w[4], bits), __funnelshift_r(w[4], w[5], bits), __funnelshift_r(w[5], w[6], bits), __funnelshift_r(w[6], w[7], bits)};
+    }
+    return r;
+}
+
+// Row t of a [T][D] matrix into shared memory by the block: the 16-byte blocks
+// that cover it, element by element where one reaches over the matrix's ends.
+// Returns the byte of `buf` at which the row starts (0..15).
+template <typename T>
+MOE_DEVINL int stage_row(const T* m, int t, int T_, int D, uint4* buf) {
+    const char *lo = reinterpret_cast<const char*>(m), *hi = lo + (size_t)T_ * D * sizeof(T);
+    const char* row = reinterpret_cast<const char*>(m + (size_t)t * D);
+    const int lead = (int)((uintptr_t)row & 15), bytes = lead + D * (int)sizeof(T);
+    const char* from = row - lead;
+    for (int j = threadIdx.x * 16; j < bytes; j += blockDim.x * 16) {
+        if (from + j >= lo && from + j + 16 <= hi) {
+            buf[j / 16] = *reinterpret_cast<const uint4*>(from + j);
+        } else {
+            for (int q = j; q < j + 16; q += sizeof(T))
+                if (from + q >= lo && from + q < hi)
+                    *reinterpret_cast<T*>(reinterpret_cast<char*>(buf) + q) = *reinterpret_cast<const T*>(from + q);
+        }
+    }
+    return lead;
+}
+
+// The copies of rows that start anywhere: the token goes to shared memory, and
+// each of its rows gets whole 16-byte blocks, shifted into place, besides its few
+// elements at either end (4,096 x 10 rows of 3,071 bf16: 54 us with the plan
+// against 88 us with single elements; of 1,535 fp32 54 us against 69 us).
+template <typename T>
+__global__ void __launch_bounds__(512) permute_rows_shifted_kernel(const T* __restrict__ x,
+                                                                   const int32_t* __restrict__ pair_row, int T_, int k,
+                                                                   int D, T* __restrict__ rows,
+                                                                   int32_t* __restrict__ row_pair) {
+    extern __shared__ __align__(16) uint4 buf[];
+    __shared__ int32_t row[kMaxTopK];
+    const int t = blockIdx.x, bytes = D * (int)sizeof(T);
+    const int lead = stage_row(x, t, T_, D, buf);       // x may be read early: see permute_rows_kernel
+    pdl_wait();
+    if (threadIdx.x < k) {
+        const int p = t * k + threadIdx.x, i = __ldg(pair_row + p);
+        row[threadIdx.x] = i;
+        if (i >= 0) row_pair[i] = p;
+    }
+    __syncthreads();
+    for (int r = 0; r < k; ++r) {
+        if (row[r] < 0) continue;
+        char* to = reinterpret_cast<char*>(rows + (size_t)row[r] * D);
+        const Row16 at(to, bytes);
+        for (int j = threadIdx.x; j < at.body; j += blockDim.x)
+            *reinterpret_cast<uint4*>(to + at.head + 16 * j) = bytes16(buf, lead + at.head + 16 * j);
+        // elements: threads 0..7 before the body, 8..15 after it
+        const int q = threadIdx.x % 8 * (int)sizeof(T) + (threadIdx.x < 8 ? 0 : bytes - at.tail);
+        if (threadIdx.x < 16 && q < (threadIdx.x < 8 ? at.head : bytes))
+            *reinterpret_cast<T*>(to + q) = *reinterpret_cast<const T*>(reinterpret_cast<const char*>(buf) + lead + q);
+    }
+}
+
 // out[t] = sum_r w[t,r] rows[row(t,r)], r ascending in fp32 (w NULL: 1).  `each`
 // threads (a power of two) take a token, each of them U packs of it, `each` packs
 // apart, and load them from all of the token's up to R rows before they add the
@@ -424,6 +508,116 @@ __global__ void __launch_bounds__(kDotThreads) unpermute_backward_kernel(const T
     if (rank == 0 && p < P) dweights[p] = dot;
 }
 
+// The same for rows that start anywhere, a block per token: dout[t] in shared
+// memory, rows and drows (which start alike: their buffers are apart by a multiple
+// of 16 bytes) in whole 16-byte blocks, four rows in flight (4,096 x 10 rows of
+// 3,071 bf16: 103 us against 168 us with single elements).
+template <typename T, typename TO>
+__global__ void __launch_bounds__(512) unpermute_backward_shifted_kernel(const TO* __restrict__ dout,
+                                                                         const T* __restrict__ rows, int n_rows,
+                                                                         const int32_t* __restrict__ pair_row,
+                                                                         const float* __restrict__ weights, int T_, int k,
+                                                                         int D, T* __restrict__ drows,
+                                                                         float* __restrict__ dweights) {
+    extern __shared__ __align__(16) uint4 buf[];
+    // of every rank: the first block's place in rows and drows, the blocks (0: no row), the first's place in buf
+    __shared__ size_t s_at[kMaxTopK];
+    __shared__ int s_body[kMaxTopK], s_from[kMaxTopK];
+    __shared__ float s_w[kMaxTopK], part[kMaxTopK][16 + 1];
+    constexpr int V = 16 / sizeof(T), B = 4, E = sizeof(T), EO = sizeof(TO);
+    const int t = blockIdx.x, bytes = D * E, lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const char* from = reinterpret_cast<const char*>(rows);
+    char* to = reinterpret_cast<char*>(drows);
+    pdl_wait();
+    const int lead = stage_row(dout, t, T_, D, buf);
+    if (threadIdx.x < kMaxTopK) {
+        const int p = t * k + threadIdx.x, i = (int)threadIdx.x < k ? __ldg(pair_row + p) : -1;
+        const size_t at = (size_t)(i < 0 ? 0 : i) * bytes;
+        const Row16 r((dweights ? from : to) + at, bytes);
+        s_at[threadIdx.x] = at + r.head;
+        s_body[threadIdx.x] = i >= 0 && i < n_rows ? r.body : 0;
+        s_from[threadIdx.x] = lead + r.head / E * EO;
+        s_w[threadIdx.x] = weights && (int)threadIdx.x < k ? __ldg(weights + p) : 1.f;
+    }
+    __syncthreads();
+    for (int r0 = 0; r0 < k; r0 += B) {
+        float dot[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) dot[b] = 0.f;
+        for (int j = threadIdx.x; j < bytes / 16; j += blockDim.x) {        // a row's blocks are this many or one less
+            uint4 y[B];
+#pragma unroll
+            for (int b = 0; b < B; ++b)
+                if (dweights && j < s_body[r0 + b]) y[b] = *reinterpret_cast<const uint4*>(from + s_at[r0 + b] + 16 * j);
+#pragma unroll
+            for (int b = 0; b < B; ++b) hold(y[b]);
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                if (j >= s_body[r0 + b]) continue;
+                float g[V];                     // the elements of dout that belong to the block
+#pragma unroll
+                for (int h = 0; h < V * EO / 16; ++h) {
+                    constexpr int W = 16 / EO;
+                    float v[W];
+                    unpack<TO, W>(bytes16(buf, s_from[r0 + b] + j * V * EO + 16 * h), v);
+#pragma unroll
+                    for (int q = 0; q < W; ++q) g[h * W + q] = v[q];
+                }
+                if (dweights) {
+                    float v[V];
+                    unpack<T, V>(y[b], v);
+#pragma unroll
+                    for (int q = 0; q < V; ++q) dot[b] = __fmaf_rn(g[q], v[q], dot[b]);
+                }
+                if (drows) {
+#pragma unroll
+                    for (int q = 0; q < V; ++q) g[q] *= s_w[r0 + b];
+                    store_f32<T, V>(reinterpret_cast<T*>(to + s_at[r0 + b] + 16 * j), g);
+                }
+            }
+        }
+        if (dweights) {
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                dot[b] = warp_sum(dot[b]);
+                if (lane == 0) part[r0 + b][w] = dot[b];
+            }
+        }
+    }
+    // the elements at the rows' ends, a warp per row: lanes 0..7 before the blocks, 8..15 after them
+    for (int r = w; r < k; r += warps) {
+        float dot = 0.f;
+        if (s_body[r] > 0 && lane < 16) {
+            const int head = (s_from[r] - lead) / EO, tail = head + s_body[r] * V;
+            const int q = lane < 8 ? lane : tail + lane - 8;
+            if (q < (lane < 8 ? head : D)) {
+                const size_t at = s_at[r] + (size_t)((q - head) * E);       // head may exceed q: the sum wraps back
+                float g[1], v[1];
+                load_f32<TO, 1>(reinterpret_cast<const TO*>(reinterpret_cast<const char*>(buf) + lead) + q, g);
+                if (dweights) {
+                    load_f32<T, 1>(reinterpret_cast<const T*>(from + at), v);
+                    dot = g[0] * v[0];
+                }
+                if (drows) {
+                    g[0] *= s_w[r];
+                    store_f32<T, 1>(reinterpret_cast<T*>(to + at), g);
+                }
+            }
+        }
+        if (dweights) {
+            dot = warp_sum(dot);
+            if (lane == 0) part[r][16] = dot;
+        }
+    }
+    if (!dweights) return;
+    __syncthreads();
+    if (threadIdx.x < k) {
+        float s = 0.f;
+        for (int i = 0; i < warps; ++i) s += part[threadIdx.x][i];
+        dweights[(size_t)t * k + threadIdx.x] = s + part[threadIdx.x][16];
+    }
+}
+
 // The least power of two >= n, in [lo, hi].
 inline int threads_for(int n, int lo, int hi) {
     while (lo < n && lo < hi) lo *= 2;
@@ -441,6 +635,9 @@ template <typename... P>
 inline bool wide_rows(int D, size_t elem, P... p) {
     return (D * elem) % 16 == 0 && (ops_aligned(p, 16) && ...);
 }
+
+// Shared memory for a row that starts anywhere, read two blocks at a time.
+inline size_t staged_bytes(int D, size_t elem) { return (D * elem + 15) / 16 * 16 + 32; }
 
 template <typename T, typename TO, int V, int U>
 cudaError_t run_unpermute(const void* rows, int n_rows, const int32_t* pair_row, const float* weights, int T_, int k,
@@ -468,6 +665,14 @@ template <typename T, typename TO, int V, int U>
 cudaError_t run_unpermute_backward(const void* dout, const void* rows, int n_rows, const int32_t* pair_row,
                                    const float* weights, int P, int k, int D, void* drows, float* dweights,
                                    cudaStream_t s) {
+    if constexpr (V == 1) {
+        const bool alike = !drows || !dweights || ((uintptr_t)drows - (uintptr_t)rows) % 16 == 0;
+        if (alike && D * (int)sizeof(T) >= kShiftBytes)
+            return launch_pdl(unpermute_backward_shifted_kernel<T, TO>, dim3(P / k),
+                              dim3(row_threads(D * (int)sizeof(T) / 16)), staged_bytes(D, sizeof(TO)), s,
+                              static_cast<const TO*>(dout), static_cast<const T*>(rows), n_rows, pair_row, weights, P / k,
+                              k, D, static_cast<T*>(drows), dweights);
+    }
     const int need = (D + V * U - 1) / (V * U);
     auto go = [&](auto e) {
         constexpr int EACH = decltype(e)::value;
@@ -520,6 +725,9 @@ moe_status launch_permute(const int32_t* ids, int T_, int k, int E, const int32_
                                      (size_t)kPlanWarps * ((E + 1) / 2 * 2) * 4, s, ids, P, E, slot_table, n_slots, offsets, pair_row,
                                      x ? nullptr : row_pair);
     if (e != cudaSuccess || !x) return ops_status(e);
+    if (!wide && D * (int)sizeof(T) >= kShiftBytes)
+        return ops_status(launch_pdl(permute_rows_shifted_kernel<T>, dim3(T_), dim3(row_threads(D / V)), staged_bytes(D, sizeof(T)),
+                                     s, x, (const int32_t*)pair_row, T_, k, D, rows, row_pair));
     auto kernel = wide ? permute_rows_kernel<T, V> : permute_rows_kernel<T, 1>;
     return ops_status(launch_pdl(kernel, dim3(T_), dim3(row_threads(wide ? D / V : D)), 0, s, x,
                                  (const int32_t*)pair_row, k, D, rows, row_pair));

@@ -61,6 +61,13 @@ CASES = [
     (700, 10, 512, 72, BF, "distinct", None, 0),
     (2049, 10, 512, 24, BF, "distinct", 0.62, 0),
     (5000, 16, 1000, 8, HF, "wild", 0.3, 0),
+    # rows that start anywhere, moved in shifted 16-byte blocks
+    (900, 6, 31, 203, BF, "wild", 0.5, 0),
+    (1100, 4, 16, 67, FL, "distinct", None, 1),
+    (600, 7, 40, 130, HF, "distinct", 0.4, 3),
+    (1, 16, 16, 8191, BF, "distinct", None, 1),
+    (300, 16, 1024, 130, FL, "distinct", None, 0),
+    (7, 9, 12, 8190, FL, "wild", None, 2),
 ]
 
 
