@@ -36,6 +36,12 @@ MOE_DEVINL Pack<T, V> load_pack(const T* p) {
     if constexpr (V * sizeof(T) == 2) return *reinterpret_cast<const uint16_t*>(p);
     else return *reinterpret_cast<const Pack<T, V>*>(p);
 }
+// Past the L1 cache: for what is read before the kernel's dependency wait.
+template <typename T, int V>
+MOE_DEVINL Pack<T, V> load_pack_l2(const T* p) {
+    if constexpr (V * sizeof(T) == 2) return __ldcg(reinterpret_cast<const unsigned short*>(p));
+    else return __ldcg(reinterpret_cast<const Pack<T, V>*>(p));
+}
 template <typename T, int V>
 MOE_DEVINL void store_pack(T* p, const Pack<T, V>& a) {
     if constexpr (V * sizeof(T) == 2) *reinterpret_cast<uint16_t*>(p) = (uint16_t)a;

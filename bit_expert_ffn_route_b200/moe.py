@@ -306,40 +306,46 @@ def _dtype(name, t):
     return _DTYPES[t.dtype]
 
 
+# Looked up once: these five checks of each tensor are half of a decode step's call.
+_address, _device_index, _contiguous = torch.Tensor.data_ptr, torch.Tensor.get_device, torch.Tensor.is_contiguous
+
+
 def _arg(name, t, dtype, shape, device):
-    """The device address of a contiguous tensor of this type and shape (None for None)."""
+    """The device address of a contiguous tensor of this type and shape on this device (None for None)."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, not "
+    if t.dtype is not dtype or t.shape != shape or _device_index(t) != device or not _contiguous(t):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on device {device}, not "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', strided'}")
-    return t.data_ptr()
+    return _address(t)
 
 
 def _call(fn, device, stream, *args):
-    if device.type != "cuda":
-        raise ValueError(f"{fn} takes CUDA tensors, not tensors on {device}")
-    if stream is not None and stream.device != device:
-        raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on {device}")
-    index = device.index
-    if index != torch.cuda.current_device():
+    """One call on CUDA device `device` (an index; -1: the tensors are not on one)."""
+    if device < 0:
+        raise ValueError(f"{fn} takes CUDA tensors")
+    if stream is not None and stream.device.index != device:
+        raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on cuda:{device}")
+    if device != torch.cuda.current_device():
         with torch.cuda.device(device):
             return _call(fn, device, stream, *args)
     # the handle alone: torch.cuda.current_stream() makes a Stream object, 3 us of a decode step's call
-    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    handle = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
     st = getattr(_lib or lib(), fn)(*args, handle)
     if st != MOE_OK:
         raise MoeError(fn, st)
 
 
-def moe_permute(ids, E, offsets, pair_row, row_pair, x=None, rows=None, slot_table=None, n_slots=0, stream=None):
+def moe_permute(ids, E, offsets, pair_row, row_pair, x=None, rows=None, slot_table=None, n_slots=None, stream=None):
     """Tokens sorted by expert: rows[i] = x[row_pair[i] // k], grouped by expert (all pairs, or with slot_table the
-    missed ones).  Without x and rows only the plan (offsets, pair_row, row_pair) is made."""
+    missed ones, given n_slots as well).  Without x and rows only the plan (offsets, pair_row, row_pair) is made."""
     T, k = ids.shape
-    dev = ids.device
+    if slot_table is not None and n_slots is None:
+        raise ValueError("moe_permute: slot_table comes with the pool's n_slots")
+    dev = _device_index(ids)
     dt, D = (MOE_BF16, 1) if x is None else (_dtype("x", x), x.shape[-1])
     _call("moe_permute", dev, stream, _arg("ids", ids, _I32, (T, k), dev), T, k, E,
-          _arg("slot_table", slot_table, _I32, (E,), dev), n_slots,
+          _arg("slot_table", slot_table, _I32, (E,), dev), n_slots or 0,
           None if x is None else _arg("x", x, x.dtype, (T, D), dev), D, dt,
           None if x is None and rows is None else _arg("rows", rows, rows.dtype if x is None else x.dtype, (T * k, D),
                                                        dev),
@@ -351,7 +357,7 @@ def moe_permute_backward(drows, pair_row, dx, stream=None):
     """dx[t] = the sum of drows over token t's rows."""
     T, k = pair_row.shape
     n, D = drows.shape
-    dev = drows.device
+    dev = _device_index(drows)
     _call("moe_permute_backward", dev, stream, _arg("drows", drows, drows.dtype, (n, D), dev), n,
           _arg("pair_row", pair_row, _I32, (T, k), dev), T, k, D, _dtype("drows", drows),
           _arg("dx", dx, drows.dtype, (T, D), dev))
@@ -361,7 +367,7 @@ def moe_unpermute(rows, pair_row, out, weights=None, stream=None):
     """out[t] = the sum of weights[t, r] * rows[pair_row[t, r]]; out of rows' type or float32 (a miss_partial)."""
     T, k = pair_row.shape
     n, D = rows.shape
-    dev = rows.device
+    dev = _device_index(rows)
     _call("moe_unpermute", dev, stream, _arg("rows", rows, rows.dtype, (n, D), dev), n,
           _arg("pair_row", pair_row, _I32, (T, k), dev), _arg("weights", weights, _F32, (T, k), dev), T, k, D,
           _dtype("rows", rows), _arg("out", out, out.dtype, (T, D), dev), _dtype("out", out))
@@ -374,7 +380,7 @@ def moe_unpermute_backward(dout, pair_row, drows=None, rows=None, weights=None, 
     if like is None:
         raise ValueError("moe_unpermute_backward writes drows, dweights (from rows), or both")
     n, D = like.shape
-    dev = dout.device
+    dev = _device_index(dout)
     _call("moe_unpermute_backward", dev, stream, _arg("dout", dout, dout.dtype, (T, D), dev), _dtype("dout", dout),
           _arg("rows", rows, like.dtype, (n, D), dev), n, _arg("pair_row", pair_row, _I32, (T, k), dev),
           _arg("weights", weights, _F32, (T, k), dev), T, k, D, _dtype("rows", like),
@@ -390,7 +396,7 @@ def moe_route_backward(dgates, gates, ids, x, Wr, offsets, row_pair, dlogits, ws
     """Gradient of moe_route_topk's gates; offsets and row_pair are moe_permute's of the same ids (no slot_table)."""
     T, k = ids.shape
     E, D = Wr.shape
-    dev = ids.device
+    dev = _device_index(ids)
     _call("moe_route_backward", dev, stream, _arg("dgates", dgates, _F32, (T, k), dev),
           _arg("gates", gates, _F32, (T, k), dev), _arg("ids", ids, _I32, (T, k), dev),
           _arg("x", x, _BF16, (T, D), dev), _arg("Wr", Wr, _BF16, (E, D), dev),
@@ -412,7 +418,7 @@ def moe_block_norm(y, x_out=None, residual=None, alpha=1.0, gate=None, gate_mode
     """x_out = alpha * residual + gate * norm(y) * w_post (y itself without w_post); normed = norm(x_out) * w_next.
     gate_mode: 'channel' (gate [D]) or 'token' (gate [T])."""
     T, D = y.shape
-    dev, dt = y.device, y.dtype
+    dev, dt = _device_index(y), y.dtype
     mode, gs = _gate(gate, gate_mode, T, D)
     _call("moe_block_norm", dev, stream, _arg("y", y, dt, (T, D), dev), _arg("residual", residual, dt, (T, D), dev),
           _arg("gate", gate, _F32, gs, dev), mode, alpha, _arg("w_post", w_post, _F32, (D,), dev),
@@ -430,7 +436,7 @@ def moe_block_norm_backward(dx_out, dnormed, x_out, y, dy, ws, dresidual=None, a
                             rstd_next=None, stream=None):
     """Gradients of moe_block_norm; the arguments left None there stay None here, as do gradients not wanted."""
     T, D = dy.shape
-    dev, dt = dy.device, dy.dtype
+    dev, dt = _device_index(dy), dy.dtype
     mode, gs = _gate(gate, gate_mode, T, D)
     _call("moe_block_norm_backward", dev, stream, _arg("dx_out", dx_out, dt, (T, D), dev),
           _arg("dnormed", dnormed, dt, (T, D), dev), _arg("x_out", x_out, dt, (T, D), dev),

@@ -218,6 +218,35 @@ def test_rows_outside_the_buffer_are_no_rows():
     assert (dw[2] == 0).all() and (dw[4] == 0).all() and dw[0, 1] == 0
 
 
+def test_buffers_that_start_differently():
+    """rows and drows apart by less than 16 bytes: their blocks of 16 do not coincide."""
+    T, k, E, D = 90, 3, 7, 333
+    ids, _, _, d_ids, _ = setup((T, k, E, D, BF, "distinct", None, 0), 3)
+    o, pr, rp, _ = buffers(T, k, E)
+    moe.moe_permute(d_ids, E, o, pr, rp)
+    rows, dout, w = shifted((T * k, D), BF, 1, seed=1), shifted((T, D), BF, 2, seed=2), torch.rand(T, k, device="cuda")
+    got = []
+    for off in (1, 3):
+        drows, dw = shifted((T * k, D), BF, off, fill=5.0), torch.empty(T, k, device="cuda")
+        moe.moe_unpermute_backward(dout, pr, drows, rows=rows, weights=w, dweights=dw)
+        g, held, wdw, wmag = ref.unpermute_backward(f64(dout), f64(rows), pr.cpu().numpy(), f64(w))
+        check(drows, g, stored(g, U32 * np.abs(g), BF), "drows")
+        check(dw, wdw, 1.01 * (D + 1) * U32 * wmag, "dweights")
+        got.append(drows)
+    assert torch.equal(*got)
+
+
+def test_no_rows():
+    """No row at all (an empty buffer): sums are zero, so are the weights' gradients."""
+    pr = torch.zeros(5, 2, dtype=torch.int32, device="cuda")
+    rows, out = torch.empty(0, 40, device="cuda"), torch.full((5, 40), 3.0, device="cuda")
+    moe.moe_unpermute(rows, pr, out)
+    assert (out == 0).all()
+    dw = torch.full((5, 2), 3.0, device="cuda")
+    moe.moe_unpermute_backward(out, pr, rows=rows, dweights=dw)
+    assert (dw == 0).all()
+
+
 def test_no_tokens():
     ids = torch.zeros(0, 2, dtype=torch.int32, device="cuda")
     o = torch.full((5,), 3, dtype=torch.int32, device="cuda")

@@ -146,6 +146,8 @@ def test_binding_refuses_tensors_it_cannot_pass():
         a = dict(ids=ids, x=x, rows=rows) | bad
         with pytest.raises(ValueError):
             moe.moe_permute(a["ids"], 5, *plan, x=a["x"], rows=a["rows"])
+    with pytest.raises(ValueError, match="n_slots"):
+        moe.moe_permute(ids, 5, *plan, x=x, rows=rows, slot_table=i32(5))
     with pytest.raises(ValueError, match="offsets"):
         moe.moe_permute(ids, 6, *plan, x=x, rows=rows)
     with pytest.raises(ValueError, match="weights"):
