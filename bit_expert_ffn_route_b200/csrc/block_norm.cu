@@ -4,12 +4,17 @@
 //   r = rsqrt(mean(v^2) + eps)
 // Each element of y and the residual is read once and each of x_out and normed
 // written once; a token stays in registers between the two norms.  Gradients
-// likewise: four rows in, two out.  HBM bounds both.
+// likewise: four rows in, two out.  HBM is the floor of both; what bounds them is
+// the chain of a token's steps (rows out of shared memory, a sum over the block's
+// warps, the rest) with as many warps as the registers leave.  4,096 tokens of
+// 3,072 bf16: 20 us forward (100 MB, 5.1 TB/s) and 38 us backward (151 MB, 4.0
+// TB/s; 31 us of it the tokens, the rest the join of the partial sums).
 //
 // Threads: a group of whole warps takes a token, each thread the same columns of
-// every token it takes, so that weights and the sums over tokens stay in its
-// registers; short rows put several groups in a block.  Groups walk over the
-// tokens and fetch the rows of their next tokens with cp.async while they work.
+// every token it takes, so that the sums over tokens stay in its registers; short
+// rows put several groups in a block.  Groups walk over the tokens and fetch the
+// rows of their next tokens with cp.async while they work (loads at the start of
+// a block per token: 26 and 71 us).
 // Rows of whole 16-byte packs: a thread copies just what it will read itself, so
 // no barrier guards the copies.  Other rows start anywhere: the 16-byte blocks
 // that cover the row are copied (elements where such a block reaches over the
@@ -24,7 +29,8 @@
 namespace moe {
 namespace {
 
-constexpr int kNormParts = 296;        // most blocks of the backward pass: two per SM, a partial of each sum over tokens from every one
+constexpr int kNormParts = 296;        // most blocks of the backward pass, two per SM: each leaves a partial of every
+                                       // sum over tokens
 constexpr int kNormThreads = 384;      // threads that the groups of a block fill, about
 constexpr int kMaxGroups = 12;         // named barriers 1..12
 constexpr int kMaxDynamic = 227 * 1024;
@@ -138,7 +144,8 @@ constexpr int kSumFloats = 256;
 
 // How rows lie: they start anywhere (ANY), they are of whole 16-byte packs
 // (WIDE), or besides every thread of the group has all its columns and the call
-// has every operand but a token gate (FULL: no test of these in the token's path).
+// has every operand but a token gate (FULL: no test of these in the token's path;
+// 4,096 x 3,072 bf16 forward 19.2 us against 21.3 us, backward 38 against 40).
 enum { ANY, WIDE, FULL };
 
 // Thread `rank` of a group of `size` owns N elements of a row: packs of V, at
@@ -231,7 +238,8 @@ struct Ring {
 
 // A thread's factors of its columns: w_post times a channel gate, and w_next
 // (1 where absent).  Kept in shared memory, a thread's N values in packs of four
-// that neighbouring threads hold next to one another, or in registers.
+// that neighbouring threads hold next to one another (in registers the backward
+// pass spilled: 44 us against 40), or in registers where it is full.
 template <int N, bool KEPT>
 struct Factors {
     float4* at;                                 // [2][N / 4][threads per token]
@@ -297,13 +305,13 @@ struct NormArgs {
 template <typename T, int N, int STAGES, int THREADS, int KIND>
 __global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 3 : 1)
     block_norm_kernel(const __grid_constant__ NormArgs a) {
-    extern __shared__ __align__(16) float dyn[];        // sums, then rings, of every group
+    extern __shared__ __align__(16) float dyn[];        // the groups' sums, the factors, the groups' rings
     const int groups = blockDim.x / a.group, g = threadIdx.x / a.group, rank = threadIdx.x % a.group;
     const int step = gridDim.x * groups, t0 = blockIdx.x * groups + g;
     Group grp{g, rank, a.group, dyn + g * kSumFloats};
     const Cols<T, N, KIND> col{rank, a.group, a.D};
-    Ring<T, N, 2, STAGES, KIND, NormArgs> in{a, col,
-                                             reinterpret_cast<char*>(dyn + groups * kSumFloats + 2 * N * a.group) + g * STAGES * 2 * a.pitch};
+    char* rings = reinterpret_cast<char*>(dyn + groups * kSumFloats + 2 * N * a.group);
+    Ring<T, N, 2, STAGES, KIND, NormArgs> in{a, col, rings + g * STAGES * 2 * a.pitch};
     const uint32_t skip = step * a.D * (uint32_t)sizeof(T);
     uint32_t at = t0 * a.D * (uint32_t)sizeof(T);       // the token's offset in every matrix
     pdl_wait();
@@ -353,13 +361,14 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 3 : 1)
         } else if (KIND == ANY) {
             grp.sync();                         // all of the group have read the token
         }
+        if (KIND == ANY && a.group == 32) __syncwarp();     // the sums above had no barrier
         in.fetch(at + STAGES * skip, t + STAGES * step < a.T);
         at += skip;
     }
 }
 
 struct NormGradArgs {
-    const void* rows[4];                        // x_out and dnormed (null without w_next), dx_out or null, y (null if not read)
+    const void* rows[4];                        // x_out, dnormed (null without w_next), dx_out or null, y (null: not read)
     const float* gate;
     int gate_mode;
     float alpha;
@@ -379,9 +388,9 @@ struct NormGradArgs {
 //   SMEM: the sums over tokens are kept in shared memory, for rows too wide for
 //   the registers.
 template <typename T, int N, int STAGES, int THREADS, bool SMEM, int KIND>
-__global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 2 : 1) 
+__global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 2 : 1)
     block_norm_backward_kernel(const __grid_constant__ NormGradArgs a) {
-    extern __shared__ __align__(16) float dyn[];        // the groups' sums, [2][D] sums over tokens, the groups' rings
+    extern __shared__ __align__(16) float dyn[];        // the groups' sums, [2][D] over tokens, the factors, the rings
     const int groups = blockDim.x / a.group, g = threadIdx.x / a.group, rank = threadIdx.x % a.group;
     const int step = gridDim.x * groups, t0 = blockIdx.x * groups + g;
     Group grp{g, rank, a.group, dyn + g * kSumFloats};
@@ -389,8 +398,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 2 : 1)
     constexpr bool KEPT = kept_factors<T>(SMEM);
     float* sums = dyn + groups * kSumFloats;            // with SMEM or several groups
     const int sums_floats = SMEM || groups > 1 ? (2 * a.D + 3) / 4 * 4 : 0;
-    Ring<T, N, 4, STAGES, KIND, NormGradArgs> in{a, col,
-                                                 reinterpret_cast<char*>(sums + sums_floats + (KEPT ? 0 : 2 * N * a.group)) + g * STAGES * 4 * a.pitch};
+    char* rings = reinterpret_cast<char*>(sums + sums_floats + (KEPT ? 0 : 2 * N * a.group));
+    Ring<T, N, 4, STAGES, KIND, NormGradArgs> in{a, col, rings + g * STAGES * 4 * a.pitch};
     const uint32_t skip = step * a.D * (uint32_t)sizeof(T);
     uint32_t at = t0 * a.D * (uint32_t)sizeof(T);
     constexpr int M = SMEM ? 2 : N;
@@ -456,6 +465,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 2 : 1)
             s2 = dot(m, xh);
         }
         grp.sum3(s0, s1, s2);
+        if (KIND == ANY && a.group == 32) __syncwarp();     // the sums had no barrier
         in.fetch(at + STAGES * skip, t + STAGES * step < a.T);  // all of the group have read the token
         const float rc1 = rx * s0 * inv, sq = __fmaf_rn(-rc1, s2, s1);
         const float c2 = post ? gt * sq * inv : 0.f;
@@ -556,7 +566,8 @@ cudaError_t run_norm(NormArgs a, cudaStream_t s) {
     const NormShape n(a.D, N, sizeof(T), KIND != ANY);
     static std::atomic<uint64_t> set{0};
     if (!once_per_device(set, [&] {
-            return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic) == cudaSuccess;
+            return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic) ==
+                   cudaSuccess;
         }))
         return cudaErrorUnknown;
     a.group = n.group;
@@ -571,7 +582,8 @@ cudaError_t run_norm_backward(NormGradArgs a, int* blocks, cudaStream_t s) {
     const NormShape n(a.D, N, sizeof(T), KIND != ANY);
     static std::atomic<uint64_t> set{0};
     if (!once_per_device(set, [&] {
-            return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic) == cudaSuccess;
+            return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic) ==
+                   cudaSuccess;
         }))
         return cudaErrorUnknown;
     a.group = n.group;
@@ -579,8 +591,9 @@ cudaError_t run_norm_backward(NormGradArgs a, int* blocks, cudaStream_t s) {
     const int sms = device_sm_count() < kNormParts / 2 ? device_sm_count() : kNormParts / 2;
     *blocks = n.blocks(a.T, THREADS == kNormThreads ? 2 * sms : sms);
     const size_t sums = SMEM || n.groups > 1 ? (size_t)(2 * a.D + 3) / 4 * 16 : 0;
+    const size_t factors = kept_factors<T>(SMEM) ? 0 : (size_t)n.group * N * 8;
     return launch_pdl(kernel, dim3(*blocks), dim3(n.group * n.groups),
-                      sums + (kept_factors<T>(SMEM) ? 0 : (size_t)n.group * N * 8) + (size_t)n.groups * (kSumFloats * 4 + STAGES * 4 * n.pitch), s, a);
+                      sums + factors + (size_t)n.groups * (kSumFloats * 4 + STAGES * 4 * n.pitch), s, a);
 }
 
 // A thread has 16 bytes of a row (twice that for fp32 rows beyond 4,096).  Blocks
@@ -648,12 +661,16 @@ extern "C" moe_status moe_block_norm(const void* y, const void* residual, const 
     const bool wide = (D * es) % 16 == 0 && ops_aligned(y, 16) && ops_aligned(residual, 16) && ops_aligned(x_out, 16) &&
                       ops_aligned(normed, 16) && ops_aligned(w_post, 16) && ops_aligned(w_next, 16) &&
                       (gate_mode != MOE_GATE_CHANNEL || ops_aligned(gate, 16));
-    const bool full = wide && whole_groups(D, es) && residual && w_post && w_next && x_out && gate_mode != MOE_GATE_TOKEN;
-    const NormArgs a{{y, residual}, gate, gate_mode, alpha, w_post, w_next, eps, T, D, 0, 0, x_out, normed, rstd_post, rstd_next};
+    const bool full =
+        wide && whole_groups(D, es) && residual && w_post && w_next && x_out && gate_mode != MOE_GATE_TOKEN;
+    const NormArgs a{{y, residual}, gate, gate_mode, alpha, w_post, w_next,   eps,
+                     T,             D,    0,         0,     x_out,  normed,   rstd_post, rstd_next};
     cudaStream_t s = (cudaStream_t)stream;
     return with_dtype(dtype, [&](auto e) {
         using Tp = decltype(e);
-        return ops_status(full ? pick_norm<Tp, FULL>(a, s) : wide ? pick_norm<Tp, WIDE>(a, s) : pick_norm<Tp, ANY>(a, s));
+        return ops_status(full   ? pick_norm<Tp, FULL>(a, s)
+                          : wide ? pick_norm<Tp, WIDE>(a, s)
+                                 : pick_norm<Tp, ANY>(a, s));
     });
 }
 
@@ -699,7 +716,8 @@ extern "C" moe_status moe_block_norm_backward(const void* dx_out, const void* dn
                       (gate_mode != MOE_GATE_CHANNEL || ops_aligned(gate, 16));
     const bool per_token = gate_mode == MOE_GATE_TOKEN;
     const bool full = wide && whole_groups(D, es) && dx_out && w_post && w_next && dresidual && !per_token;
-    const NormGradArgs a{{w_next ? x_out : nullptr, w_next ? dnormed : nullptr, dx_out, w_post || dgate ? y : nullptr}, gate, gate_mode, alpha, w_post, rstd_post, w_next, rstd_next, T, D, 0, 0, dy, dresidual,
+    const NormGradArgs a{{w_next ? x_out : nullptr, w_next ? dnormed : nullptr, dx_out, w_post || dgate ? y : nullptr},
+                         gate, gate_mode, alpha, w_post, rstd_post, w_next, rstd_next, T, D, 0, 0, dy, dresidual,
                          per_token ? dgate : nullptr, dw_next != nullptr, dw_post || dgate_cols,
                          static_cast<float*>(ws)};
     int blocks = 0;
@@ -710,6 +728,6 @@ extern "C" moe_status moe_block_norm_backward(const void* dx_out, const void* dn
                                  : pick_norm_backward<Tp, ANY>(a, &blocks, s));
     });
     if (st != MOE_OK || (!dw_next && !dw_post && !dgate_cols)) return st;
-    return ops_status(launch_pdl(block_norm_join_kernel, dim3((D + 31) / 32, 2), dim3(256), 0, s, (const float*)ws, blocks,
-                                 D, w_post, per_token ? nullptr : gate, dw_next, dw_post, dgate_cols));
+    return ops_status(launch_pdl(block_norm_join_kernel, dim3((D + 31) / 32, 2), dim3(256), 0, s, (const float*)ws,
+                                 blocks, D, w_post, per_token ? nullptr : gate, dw_next, dw_post, dgate_cols));
 }

@@ -66,15 +66,16 @@ MOE_DEVINL int block_scan(int v, int* wsum) {
 // The plan: a stable counting sort of the P pairs by expert, in one cluster.
 // Warp w of block b owns the pairs of segment (b, w), 32 at a time in order.
 // Lanes with the same expert find one another by a ballot for each bit of the
-// expert's number (a round of 8 warps per scheduler takes 1,400 clocks so,
-// 1,960 with __match_any_sync); the first of them adds their number to the
+// expert's number (with 32 warps per SM a round took 1,430 clocks so and 1,960
+// with __match_any_sync); the first of them adds their number to the
 // warp's counter of that expert and tells the others what it held, so that every
 // pair knows its rank among the warp's pairs of its expert.  An exclusive scan
 // over (expert, block, warp) gives the ranks their first row.  A chain of
 // latencies bounds it, so the ids of 8 rounds are loaded together, and the ranks
 // of the first 8 rounds stay in registers (those of longer segments wait in
 // pair_row): one walk does all the matching.  row_pair null: the next kernel
-// writes it (scattered words, too many for 8 SMs: 3 us of 40,960 pairs).
+// writes it (scattered words, which few SMs write slowly).  40,960 pairs take 8 us
+// alone, 6 us in front of the copies; a cluster of 8 blocks took 11 us.
 __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThreads)
     permute_plan_kernel(const int32_t* __restrict__ ids, int P, int E, const int32_t* __restrict__ slot_table,
                         int n_slots, int32_t* __restrict__ offsets, int32_t* __restrict__ pair_row,
@@ -133,6 +134,7 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
                 mine[key[i]] = held + __popc(peers);
             }
             rank[i] = __shfl_sync(0xffffffffu, held, leader) + __popc(peers & ((1u << lane) - 1u));
+            __syncwarp();                       // the counter is read by another lane next
             const int p = p0 + (i0 + i) * 32;
             if (rounds > kPlanHeld && p < P) pair_row[p] = rank[i];
         }
@@ -264,9 +266,10 @@ __global__ void __launch_bounds__(kSmallThreads) permute_small_kernel(
     scatter_token<T, V>(x, t, row, k, D, rows, threadIdx.x * V);
 }
 
-// The copies behind the plan, and row_pair.  The first columns of x are read while the plan is
-// still made: its blocks let this kernel start once they have waited for the
-// kernels that may have written x.
+// The copies behind the plan, and row_pair.  The first columns of x are read while
+// the plan is still made: its blocks let this kernel start once they have waited
+// for the kernels that may have written x.  4,096 tokens x 10 x 3,072 bf16: 44 us,
+// 277 MB at 6.3 TB/s.
 template <typename T, int V>
 __global__ void __launch_bounds__(512) permute_rows_kernel(const T* __restrict__ x,
                                                            const int32_t* __restrict__ pair_row, int k, int D,
@@ -301,20 +304,23 @@ struct Row16 {
 
 // 16 bytes from byte `at` (any) of a buffer in shared memory; at % 16 is the same
 // in all lanes.
+template <int Q>
+MOE_DEVINL uint4 shifted_words(const uint32_t (&w)[8], int bits) {
+    return {__funnelshift_r(w[Q], w[Q + 1], bits), __funnelshift_r(w[Q + 1], w[Q + 2], bits),
+            __funnelshift_r(w[Q + 2], w[Q + 3], bits), __funnelshift_r(w[Q + 3], w[Q + 4], bits)};
+}
 MOE_DEVINL uint4 bytes16(const uint4* buf, int at) {
     const uint4 a = buf[at / 16];
     if (at % 16 == 0) return a;
     const uint4 b = buf[at / 16 + 1];
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     const int bits = at % 4 * 8;
-    uint4 r;
     switch (at % 16 / 4) {
-        case 0: r = {w[0], w[1], w[2], w[3]}; if (bits) r = {__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits)}; break;
-        case 1: r = {__funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits), __funnelshift_r(w[4], w[5], bits)}; break;
-        case 2: r = {__funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits), __funnelshift_r(w[4], w[5], bits), __funnelshift_r(w[5], w[6], bits)}; break;
-        default: r = {__funnelshift_r(w[3], w[4], bits), __funnelshift_r(w[4], w[5], bits), __funnelshift_r(w[5], w[6], bits), __funnelshift_r(w[6], w[7], bits)};
+        case 0: return shifted_words<0>(w, bits);
+        case 1: return shifted_words<1>(w, bits);
+        case 2: return shifted_words<2>(w, bits);
+        default: return shifted_words<3>(w, bits);
     }
-    return r;
 }
 
 // Row t of a [T][D] matrix into shared memory by the block: the 16-byte blocks
@@ -373,11 +379,12 @@ __global__ void __launch_bounds__(512) permute_rows_shifted_kernel(const T* __re
 }
 
 // out[t] = sum_r w[t,r] rows[row(t,r)], r ascending in fp32 (w NULL: 1).  `each`
-// threads (a power of two) take a token, each of them U packs of it, `each` packs
-// apart, and load them from all of the token's up to R rows before they add the
-// first; short rows put several tokens in a block.  EACH: `each` as a constant
-// where U > 1, so that a thread's packs differ by constant offsets (with `each` in
-// a register 20,011 x 3 x 1,001 fp32 took 72 us instead of 58).
+// threads take a token, each of them U packs of it, `each` packs apart, and load
+// them from all of the token's up to R rows before they add the first; short rows
+// put several tokens in a block.  4,096 tokens x 10 x 3,072 bf16: 45 us, 277 MB at
+// 6.1 TB/s.  EACH: `each` as a constant where U > 1, so that a thread's packs
+// differ by constant offsets (20,011 x 3 x 1,001 fp32: 53 us, 6.0 TB/s; with `each`
+// in a register 72 us).
 template <typename T, typename TO, int V, int U, int R, int EACH>
 __global__ void __launch_bounds__(kSumThreads) unpermute_kernel(const T* __restrict__ rows, int n_rows,
                                                                 const int32_t* __restrict__ pair_row,
@@ -387,8 +394,8 @@ __global__ void __launch_bounds__(kSumThreads) unpermute_kernel(const T* __restr
     __shared__ int s_row[kSumThreads / 8 * kMaxTopK];
     __shared__ float s_w[kSumThreads / 8 * kMaxTopK];
     pdl_wait();
-    const int tokens = kSumThreads / each, t0 = blockIdx.x * tokens, mine = threadIdx.x / each;
-    for (int i = threadIdx.x; i < tokens * k; i += kSumThreads) {
+    const int tokens = blockDim.x / each, t0 = blockIdx.x * tokens, mine = threadIdx.x / each;
+    for (int i = threadIdx.x; i < tokens * k; i += blockDim.x) {
         const int p = t0 * k + i;
         int row = -1;
         if (p < T_ * k) {
@@ -437,7 +444,8 @@ __global__ void __launch_bounds__(kSumThreads) unpermute_kernel(const T* __restr
 
 // drows[row(p)] = w[p] dout[t] and dw[p] = <dout[t], rows[row(p)]>: EACH threads
 // per pair, U packs in flight per thread.  The pairs of a token read dout[t] after
-// one another, so all but the first find it in the caches.
+// one another, so all but the first find it in the caches.  4,096 tokens x 10 x
+// 3,072 bf16: 83 us, 528 MB at 6.4 TB/s.
 template <typename T, typename TO, int V, int U, int EACH>
 __global__ void __launch_bounds__(kDotThreads) unpermute_backward_kernel(const TO* __restrict__ dout,
                                                                          const T* __restrict__ rows, int n_rows,
@@ -645,10 +653,13 @@ template <typename T, typename TO, int V, int U>
 cudaError_t run_unpermute(const void* rows, int n_rows, const int32_t* pair_row, const float* weights, int T_, int k,
                           int D, void* out, cudaStream_t s) {
     const int packs = (D + V - 1) / V, need = (packs + U - 1) / U;
-    const int each = U == 1 ? threads_for(need, 8, kSumThreads) : need <= 8 ? 8 : need <= 32 ? 32 : kSumThreads;
-    const dim3 grid((T_ + kSumThreads / each - 1) / (kSumThreads / each), (packs + U * each - 1) / (U * each));
+    // U == 1, long rows: a token per block, its packs dealt evenly to blocks of at most 128 threads
+    const int slices = (need + kSumThreads - 1) / kSumThreads, even = ((need + slices - 1) / slices + 31) / 32 * 32;
+    const int each = U > 1 ? (need <= 8 ? 8 : need <= 32 ? 32 : kSumThreads) : need > 64 ? even : threads_for(need, 8, 64);
+    const int tokens = kSumThreads / each;
+    const dim3 grid((T_ + tokens - 1) / tokens, (packs + U * each - 1) / (U * each));
     auto go = [&](auto kernel) {
-        return launch_pdl(kernel, grid, dim3(kSumThreads), 0, s, static_cast<const T*>(rows), n_rows, pair_row, weights,
+        return launch_pdl(kernel, grid, dim3(tokens * each), 0, s, static_cast<const T*>(rows), n_rows, pair_row, weights,
                           T_, k, D, each, static_cast<TO*>(out));
     };
     auto by_rank = [&](auto e) {
@@ -683,6 +694,9 @@ cudaError_t run_unpermute_backward(const void* dout, const void* rows, int n_row
                           static_cast<const TO*>(dout), static_cast<const T*>(rows), n_rows, pair_row, weights, P, k, D,
                           static_cast<T*>(drows), dweights);
     };
+    // Threads per pair: as many as its packs ask for, but a warp where the pairs alone fill the GPU (packs of 16 bytes,
+    // 6,000 pairs of 3,072 bf16: 16.4 us against 20.9 us with 128 threads; 240 pairs: 8.9 us with 128).  Single
+    // elements take all they can get (5,439 pairs of 2,055 fp16: 12.6 us with 256 threads, 18.2 us with 128).
     if (need <= 8) return go(std::integral_constant<int, 8>{});
     if (need <= 32 || (V > 1 && P >= kManyPairs)) return go(std::integral_constant<int, 32>{});
     if (need <= 160) return go(std::integral_constant<int, 128>{});
@@ -724,12 +738,13 @@ moe_status launch_permute(const int32_t* ids, int T_, int k, int E, const int32_
         }))
         return MOE_ERR_CUDA;
     const cudaError_t e = launch_pdl(permute_plan_kernel, dim3(kPlanBlocks), dim3(kPlanThreads),
-                                     (size_t)kPlanWarps * ((E + 1) / 2 * 2) * 4, s, ids, P, E, slot_table, n_slots, offsets, pair_row,
-                                     x ? nullptr : row_pair);
+                                     (size_t)kPlanWarps * ((E + 1) / 2 * 2) * 4, s, ids, P, E, slot_table, n_slots,
+                                     offsets, pair_row, x ? nullptr : row_pair);
     if (e != cudaSuccess || !x) return ops_status(e);
     if (!wide && D * (int)sizeof(T) >= kShiftBytes)
-        return ops_status(launch_pdl(permute_rows_shifted_kernel<T>, dim3(T_), dim3(row_threads(D / V)), staged_bytes(D, sizeof(T)),
-                                     s, x, (const int32_t*)pair_row, T_, k, D, rows, row_pair));
+        return ops_status(launch_pdl(permute_rows_shifted_kernel<T>, dim3(T_), dim3(row_threads(D / V)),
+                                     staged_bytes(D, sizeof(T)), s, x, (const int32_t*)pair_row, T_, k, D, rows,
+                                     row_pair));
     auto kernel = wide ? permute_rows_kernel<T, V> : permute_rows_kernel<T, 1>;
     return ops_status(launch_pdl(kernel, dim3(T_), dim3(row_threads(wide ? D / V : D)), 0, s, x,
                                  (const int32_t*)pair_row, k, D, rows, row_pair));

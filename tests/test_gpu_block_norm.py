@@ -92,7 +92,8 @@ def backward(a, o, dx_out, dnormed, off=0, ws=None, drop=()):
     g = {"dy": shifted((T, D), dt, off, fill=9.0), "dresidual": shifted((T, D), dt, off, fill=9.0),
          "dgate": new(a["gate"]), "dw_post": new(a["w_post"]), "dw_next": new(a["w_next"])}
     g |= {n: None for n in drop}
-    ws = torch.full((moe.block_norm_backward_workspace_size(T, D),), 255, dtype=torch.uint8, device="cuda") if ws is None else ws
+    if ws is None:                                          # no initialisation asked for
+        ws = torch.full((moe.block_norm_backward_workspace_size(T, D),), 255, dtype=torch.uint8, device="cuda")
     moe.moe_block_norm_backward(dx_out, dnormed, o["x_out"], a["y"], ws=ws, alpha=a["alpha"], gate=a["gate"],
                                 gate_mode=a["gate_mode"], w_post=a["w_post"], w_next=a["w_next"],
                                 rstd_post=o["rstd_post"], rstd_next=o["rstd_next"], **g)
@@ -142,7 +143,8 @@ def test_gradients_against_differences(mode):
     want = ref.norm_backward(f64(c), f64(d), f64(o["x_out"]), base["y"], 0.5, base.get("gate"), mode, base["w_post"],
                              base["w_next"], EPS)
     rng, h = np.random.default_rng(1), 1e-4
-    for n, out in (("y", "dy"), ("residual", "dresidual"), ("gate", "dgate"), ("w_post", "dw_post"), ("w_next", "dw_next")):
+    for n, out in (("y", "dy"), ("residual", "dresidual"), ("gate", "dgate"), ("w_post", "dw_post"),
+                   ("w_next", "dw_next")):
         if n not in base:
             continue
         v = rng.standard_normal(base[n].shape)

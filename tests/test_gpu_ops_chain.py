@@ -131,8 +131,9 @@ def test_gradients_of_a_block(T, experts):
     dx = torch.empty_like(x)
     moe.moe_permute_backward(drows, pr, dx)
     dl, dW, db = torch.empty(T, k, device="cuda"), torch.empty(E, D, device="cuda"), torch.empty(E, device="cuda")
-    moe.moe_route_backward(dgates, gates, ids, x, Wr, o, rp, dl, moe.alloc_ws(moe.route_backward_workspace_size(T, D, E, k)),
-                           dx=dx, dx_add=dx, dWr=dW, dbias=db)
+    moe.moe_route_backward(dgates, gates, ids, x, Wr, o, rp, dl,
+                           moe.alloc_ws(moe.route_backward_workspace_size(T, D, E, k)), dx=dx, dx_add=dx, dWr=dW,
+                           dbias=db)
     # the same in 64 bits
     leaf = lambda t: t.double().clone().requires_grad_(True)                # noqa: E731
     X, W, B, R, G, WP, WN = (leaf(t) for t in (x, Wr, bias, res, gate, w_post, w_next))

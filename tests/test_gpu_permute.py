@@ -197,7 +197,8 @@ def test_gradients_against_differences():
         num = (loss(r64 + da, w64) - loss(r64 - da, w64)) / 2
         assert abs(num - (f64(drows) * da).sum()) <= 4 * U32 * (np.abs(f64(drows) * da)).sum() + 1e-9
         num = (loss(r64, w64 + db) - loss(r64, w64 - db)) / 2
-        mag = sum(np.abs(c64[t] * r64[p[t, q]]).sum() * abs(db[t, q]) for t in range(T) for q in range(k) if p[t, q] >= 0)
+        mag = sum(np.abs(c64[t] * r64[p[t, q]]).sum() * abs(db[t, q])
+                  for t in range(T) for q in range(k) if p[t, q] >= 0)
         assert abs(num - (f64(dw) * db).sum()) <= 1.01 * (D + 1) * U32 * mag + 1e-9
 
 

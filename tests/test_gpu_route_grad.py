@@ -65,7 +65,8 @@ def test_against_the_formula(T, k, E, D, kind, with_add):
 def test_no_tokens():
     z = torch.zeros(0, 2, device="cuda")
     i = torch.zeros(0, 2, dtype=torch.int32, device="cuda")
-    Wr, dW, db = torch.ones(4, 256, dtype=BF, device="cuda"), torch.ones(4, 256, device="cuda"), torch.ones(4, device="cuda")
+    Wr = torch.ones(4, 256, dtype=BF, device="cuda")
+    dW, db = torch.ones(4, 256, device="cuda"), torch.ones(4, device="cuda")
     ws = moe.alloc_ws(moe.route_backward_workspace_size(0, 256, 4, 2))
     moe.moe_route_backward(z, z, i, torch.zeros(0, 256, dtype=BF, device="cuda"), Wr, torch.zeros(5, dtype=torch.int32,
                            device="cuda"), torch.zeros(0, dtype=torch.int32, device="cuda"), z, ws, dWr=dW, dbias=db)
@@ -102,7 +103,8 @@ def test_behind_the_router_against_differences(T):
         moved = np.abs(up[0] @ up[1].T + up[2] - down[0] @ down[1].T - down[2]).max() / (2 * h)
         trunc = h * h * moved ** 3 * np.abs(c64).sum()
         # moe_route_topk's gates are within 1e-6 of the 64-bit ones (its own tests), and enter twice
-        tol = (e * np.abs(v)).sum() + trunc + 1e-9 + 3e-6 * (np.abs(w) * np.abs(v)).sum() + 1e-5 * moved * np.abs(c64).sum() * 0.2
+        tol = ((e * np.abs(v)).sum() + trunc + 1e-9 + 3e-6 * (np.abs(w) * np.abs(v)).sum()
+               + 2e-6 * moved * np.abs(c64).sum())
         g = f64(got[("dx", "dWr", "dbias")[n]])
         assert abs(num - (g * v).sum()) <= tol, (n, num, (g * v).sum(), tol)
 
@@ -113,8 +115,8 @@ def test_captured(T):
     a, b = make(T, k, E, D, "distinct", 1), make(T, k, E, D, "distinct", 2)
     hold = [t.clone() for t in a[:5]]
     o, pr, rp, _ = buffers(T, k, E)
-    out = [torch.empty(T, k, device="cuda"), torch.empty(T, D, dtype=BF, device="cuda"), torch.empty(E, D, device="cuda"),
-           torch.empty(E, device="cuda")]
+    out = [torch.empty(T, k, device="cuda"), torch.empty(T, D, dtype=BF, device="cuda"),
+           torch.empty(E, D, device="cuda"), torch.empty(E, device="cuda")]
     ws = moe.alloc_ws(moe.route_backward_workspace_size(T, D, E, k))
 
     def step():
