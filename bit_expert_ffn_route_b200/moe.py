@@ -306,18 +306,20 @@ def _dtype(name, t):
     return _DTYPES[t.dtype]
 
 
-# Looked up once: these five checks of each tensor are half of a decode step's call.
-_address, _device_index, _contiguous = torch.Tensor.data_ptr, torch.Tensor.get_device, torch.Tensor.is_contiguous
+_device_index = torch.Tensor.get_device
 
 
 def _arg(name, t, dtype, shape, device):
-    """The device address of a contiguous tensor of this type and shape on this device (None for None)."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.shape != shape or _device_index(t) != device or not _contiguous(t):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on device {device}, not "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', strided'}")
-    return _address(t)
+    """The device address of a contiguous tensor of this type and shape on this device (None for None), or a
+    ValueError.  The first call puts the extension module's function (csrc/args.cpp) in this one's place."""
+    global _arg
+    try:
+        from ._args import address
+    except ImportError as e:
+        raise RuntimeError("bit_expert_ffn_route_b200/_args.so is missing or does not fit this torch: run `python -m "
+                           "bit_expert_ffn_route_b200.build --force`") from e
+    _arg = address
+    return address(name, t, dtype, shape, device)
 
 
 def _call(fn, device, stream, *args):
@@ -326,10 +328,10 @@ def _call(fn, device, stream, *args):
         raise ValueError(f"{fn} takes CUDA tensors")
     if stream is not None and stream.device.index != device:
         raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on cuda:{device}")
-    if device != torch.cuda.current_device():
+    if device != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
             return _call(fn, device, stream, *args)
-    # the handle alone: torch.cuda.current_stream() makes a Stream object, 3 us of a decode step's call
+    # the numbers alone: torch.cuda.current_device() and current_stream() (which makes an object) take 3.5 us
     handle = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
     st = getattr(_lib or lib(), fn)(*args, handle)
     if st != MOE_OK:

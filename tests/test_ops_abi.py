@@ -134,7 +134,7 @@ def test_block_norm_backward_refusals(L):
     assert call(T=0, dg=None, dwp=None, dwn=None, ws=None) == OK
 
 
-def test_binding_refuses_tensors_it_cannot_pass():
+def test_binding_refuses_tensors_it_cannot_pass(L):
     """Wrong types, shapes, strides and devices raise before any call (CPU tensors throughout: nothing runs)."""
     i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)     # noqa: E731
     ids, x, rows = i32(4, 2), torch.zeros(4, 8), torch.zeros(8, 8)
@@ -146,6 +146,10 @@ def test_binding_refuses_tensors_it_cannot_pass():
         a = dict(ids=ids, x=x, rows=rows) | bad
         with pytest.raises(ValueError):
             moe.moe_permute(a["ids"], 5, *plan, x=a["x"], rows=a["rows"])
+    with pytest.raises(ValueError, match="x must be a contiguous torch.float32 tensor .* strided"):
+        moe.moe_permute(ids, 5, *plan, x=torch.zeros(8, 4).t(), rows=rows)
+    with pytest.raises(ValueError, match="rows must be a tensor or None"):
+        moe.moe_permute(ids, 5, *plan, x=x, rows=[1.0])
     with pytest.raises(ValueError, match="n_slots"):
         moe.moe_permute(ids, 5, *plan, x=x, rows=rows, slot_table=i32(5))
     with pytest.raises(ValueError, match="offsets"):
