@@ -32,6 +32,7 @@ constexpr int kSmallPairs = 2816;          // up to here every block makes its p
 constexpr int kSmallThreads = 256;
 constexpr int kNoExpert = 0x7fffffff;
 constexpr int kShiftBytes = 256;           // rows that start anywhere: moved in shifted blocks from this length on
+constexpr int kCopyThreads = 256;          // of a block that copies several short tokens
 constexpr int kSumThreads = 128;           // of an unpermute block
 constexpr int kDotThreads = 256;           // of a block of its gradient
 constexpr int kManyPairs = 2048;           // from here on a warp per pair fills the GPU
@@ -191,16 +192,6 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
     }
 }
 
-// x[t] into the rows row[0..k), from column `c` on: the token is read once.
-template <typename T, int V>
-MOE_DEVINL void scatter_token(const T* x, int t, const int32_t* row, int k, int D, T* rows, int c) {
-    for (; c < D; c += blockDim.x * V) {
-        const Pack<T, V> a = load_pack<T, V>(x + (size_t)t * D + c);
-        for (int r = 0; r < k; ++r)
-            if (row[r] >= 0) store_pack<T, V>(rows + (size_t)row[r] * D + c, a);
-    }
-}
-
 // A small batch in one launch: block t places the pairs of token t itself, by
 // counting the pairs that come before each of them (a warp per pair, the pairs'
 // experts in shared memory), then copies its token; block T writes the offsets.
@@ -263,32 +254,47 @@ __global__ void __launch_bounds__(kSmallThreads) permute_small_kernel(
     }
     if (!x) return;
     __syncthreads();
-    scatter_token<T, V>(x, t, row, k, D, rows, threadIdx.x * V);
-}
-
-// The copies behind the plan, and row_pair.  The first columns of x are read while
-// the plan is still made: its blocks let this kernel start once they have waited
-// for the kernels that may have written x.  4,096 tokens x 10 x 3,072 bf16: 44 us,
-// 277 MB at 6.3 TB/s.
-template <typename T, int V>
-__global__ void __launch_bounds__(512) permute_rows_kernel(const T* __restrict__ x,
-                                                           const int32_t* __restrict__ pair_row, int k, int D,
-                                                           T* __restrict__ rows, int32_t* __restrict__ row_pair) {
-    __shared__ int32_t row[kMaxTopK];
-    const int t = blockIdx.x, c = threadIdx.x * V;
-    Pack<T, V> a;
-    if (c < D) a = load_pack_l2<T, V>(x + (size_t)t * D + c);
-    pdl_wait();
-    if (threadIdx.x < k) {
-        const int p = t * k + threadIdx.x, i = __ldg(pair_row + p);
-        row[threadIdx.x] = i;
-        if (i >= 0) row_pair[i] = p;
-    }
-    __syncthreads();
-    if (c < D)
+    for (int c = threadIdx.x * V; c < D; c += kSmallThreads * V) {
+        const Pack<T, V> a = load_pack<T, V>(x + (size_t)t * D + c);
         for (int r = 0; r < k; ++r)
             if (row[r] >= 0) store_pack<T, V>(rows + (size_t)row[r] * D + c, a);
-    scatter_token<T, V>(x, t, row, k, D, rows, c + blockDim.x * V);
+    }
+}
+
+// The copies behind the plan, and row_pair: a block per token, or `each` threads
+// where rows are SHORT (12,525 tokens x 12 x 32 fp16: 16 us against 22 us).  The
+// first columns of x are read while the plan is still made: its blocks let this
+// kernel start once they have waited for the kernels that may have written x.
+// (Where few pairs are taken most of those reads are for nothing; without them it
+// took longer: 22.3 us against 20.6 us of 19,284 tokens with one pair in 14 taken.)
+// 4,096 tokens x 10 x 3,072 bf16: 44 us, 277 MB at 6.3 TB/s.
+template <typename T, int V, bool SHORT>
+__global__ void __launch_bounds__(512) permute_rows_kernel(const T* __restrict__ x,
+                                                           const int32_t* __restrict__ pair_row, int T_, int k, int D,
+                                                           int each, T* __restrict__ rows,
+                                                           int32_t* __restrict__ row_pair) {
+    __shared__ int32_t row[(SHORT ? kCopyThreads / 8 : 1) * kMaxTopK];
+    const int tokens = SHORT ? kCopyThreads / each : 1, mine = SHORT ? threadIdx.x / each : 0;
+    const int step = SHORT ? each : blockDim.x, rank = SHORT ? threadIdx.x % each : threadIdx.x;
+    const int t0 = blockIdx.x * tokens, t = t0 + mine;
+    int c = rank * V;
+    Pack<T, V> a;
+    if (t < T_ && c < D) a = load_pack_l2<T, V>(x + (size_t)t * D + c);
+    pdl_wait();
+    for (int i = threadIdx.x; i < tokens * k; i += blockDim.x) {
+        const int p = t0 * k + i, r = !SHORT || p < T_ * k ? __ldg(pair_row + p) : -1;
+        row[i] = r;
+        if (r >= 0) row_pair[r] = p;
+    }
+    __syncthreads();
+    if (t >= T_) return;
+    const int32_t* to = row + mine * k;
+    while (c < D) {
+        for (int r = 0; r < k; ++r)
+            if (to[r] >= 0) store_pack<T, V>(rows + (size_t)to[r] * D + c, a);
+        c += step * V;
+        if (c < D) a = load_pack<T, V>(x + (size_t)t * D + c);
+    }
 }
 
 // Rows that start anywhere.  A matrix row's bytes from its first 16-byte boundary
@@ -539,17 +545,22 @@ __global__ void __launch_bounds__(512) unpermute_backward_shifted_kernel(const T
     const char* from = reinterpret_cast<const char*>(rows);
     char* to = reinterpret_cast<char*>(drows);
     pdl_wait();
+    int held = 0;
     const int lead = stage_row(dout, t, T_, D, buf);
     if (threadIdx.x < kMaxTopK) {
         const int p = t * k + threadIdx.x, i = (int)threadIdx.x < k ? __ldg(pair_row + p) : -1;
+        held = i >= 0 && i < n_rows;
         const size_t at = (size_t)(i < 0 ? 0 : i) * bytes;
         const Row16 r((dweights ? from : to) + at, bytes);
         s_at[threadIdx.x] = at + r.head;
-        s_body[threadIdx.x] = i >= 0 && i < n_rows ? r.body : 0;
+        s_body[threadIdx.x] = held ? r.body : 0;
         s_from[threadIdx.x] = lead + r.head / E * EO;
         s_w[threadIdx.x] = weights && (int)threadIdx.x < k ? __ldg(weights + p) : 1.f;
     }
-    __syncthreads();
+    if (!__syncthreads_or(held)) {
+        if (dweights && threadIdx.x < k) dweights[(size_t)t * k + threadIdx.x] = 0.f;
+        return;
+    }
     for (int r0 = 0; r0 < k; r0 += B) {
         float dot[B];
 #pragma unroll
@@ -745,9 +756,13 @@ moe_status launch_permute(const int32_t* ids, int T_, int k, int E, const int32_
         return ops_status(launch_pdl(permute_rows_shifted_kernel<T>, dim3(T_), dim3(row_threads(D / V)),
                                      staged_bytes(D, sizeof(T)), s, x, (const int32_t*)pair_row, T_, k, D, rows,
                                      row_pair));
-    auto kernel = wide ? permute_rows_kernel<T, V> : permute_rows_kernel<T, 1>;
-    return ops_status(launch_pdl(kernel, dim3(T_), dim3(row_threads(wide ? D / V : D)), 0, s, x,
-                                 (const int32_t*)pair_row, k, D, rows, row_pair));
+    const int packs = wide ? D / V : D;
+    const bool few = packs <= 64;
+    const int each = few ? threads_for(packs, 8, 64) : row_threads(packs), tokens = few ? kCopyThreads / each : 1;
+    auto kernel = wide ? (few ? permute_rows_kernel<T, V, true> : permute_rows_kernel<T, V, false>)
+                       : (few ? permute_rows_kernel<T, 1, true> : permute_rows_kernel<T, 1, false>);
+    return ops_status(launch_pdl(kernel, dim3((T_ + tokens - 1) / tokens), dim3(tokens * each), 0, s, x,
+                                 (const int32_t*)pair_row, T_, k, D, each, rows, row_pair));
 }
 
 bool out_dtype_ok(int dtype, int out_dtype) { return out_dtype == dtype || out_dtype == MOE_F32; }
