@@ -265,8 +265,6 @@ __global__ void __launch_bounds__(kSmallThreads) permute_small_kernel(
 // where rows are SHORT (12,525 tokens x 12 x 32 fp16: 16 us against 22 us).  The
 // first columns of x are read while the plan is still made: its blocks let this
 // kernel start once they have waited for the kernels that may have written x.
-// (Where few pairs are taken most of those reads are for nothing; without them it
-// took longer: 22.3 us against 20.6 us of 19,284 tokens with one pair in 14 taken.)
 // 4,096 tokens x 10 x 3,072 bf16: 44 us, 277 MB at 6.3 TB/s.
 template <typename T, int V, bool SHORT>
 __global__ void __launch_bounds__(512) permute_rows_kernel(const T* __restrict__ x,
@@ -279,21 +277,29 @@ __global__ void __launch_bounds__(512) permute_rows_kernel(const T* __restrict__
     const int t0 = blockIdx.x * tokens, t = t0 + mine;
     int c = rank * V;
     Pack<T, V> a;
-    if (t < T_ && c < D) a = load_pack_l2<T, V>(x + (size_t)t * D + c);
+    if ((!SHORT || t < T_) && c < D) a = load_pack_l2<T, V>(x + (size_t)t * D + c);
     pdl_wait();
-    for (int i = threadIdx.x; i < tokens * k; i += blockDim.x) {
-        const int p = t0 * k + i, r = !SHORT || p < T_ * k ? __ldg(pair_row + p) : -1;
-        row[i] = r;
+    if constexpr (SHORT) {
+        for (int i = threadIdx.x; i < tokens * k; i += blockDim.x) {
+            const int p = t0 * k + i, r = p < T_ * k ? __ldg(pair_row + p) : -1;
+            row[i] = r;
+            if (r >= 0) row_pair[r] = p;
+        }
+    } else if (threadIdx.x < k) {
+        const int p = t * k + threadIdx.x, r = __ldg(pair_row + p);
+        row[threadIdx.x] = r;
         if (r >= 0) row_pair[r] = p;
     }
     __syncthreads();
-    if (t >= T_) return;
+    if (SHORT && t >= T_) return;
     const int32_t* to = row + mine * k;
-    while (c < D) {
+    if (c < D)
         for (int r = 0; r < k; ++r)
             if (to[r] >= 0) store_pack<T, V>(rows + (size_t)to[r] * D + c, a);
-        c += step * V;
-        if (c < D) a = load_pack<T, V>(x + (size_t)t * D + c);
+    for (c += step * V; c < D; c += step * V) {
+        a = load_pack<T, V>(x + (size_t)t * D + c);
+        for (int r = 0; r < k; ++r)
+            if (to[r] >= 0) store_pack<T, V>(rows + (size_t)to[r] * D + c, a);
     }
 }
 
