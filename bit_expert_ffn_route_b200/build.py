@@ -1,5 +1,5 @@
 """Build libmoe.so (the CUDA library behind include/moe.h) for sm_100a, and the
-binding's argument check (_args.so, a Python extension module), in-tree.
+native binding of moe_ops.h (_ops.so, a Python extension module), in-tree.
 
     python -m bit_expert_ffn_route_b200.build [--force]
 
@@ -19,7 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
-ARGS_SRC, ARGS = os.path.join(CSRC, "args.cpp"), os.path.join(HERE, "_args.so")
+OPS_SRC, OPS = os.path.join(CSRC, "binding.cpp"), os.path.join(HERE, "_ops.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -41,16 +41,17 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _args_command():
+def _ops_command():
     import sysconfig
 
     import torch
-    root = os.path.join(os.path.dirname(torch.__file__), "include")
-    include = [root, os.path.join(root, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"]]
+    at = os.path.dirname(torch.__file__)
+    include = [os.path.join(at, "include"), os.path.join(at, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
-            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
-            *(f"-isystem{i}" for i in include), ARGS_SRC, "-o", ARGS,
-            "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE,
+            *(f"-isystem{i}" for i in include), OPS_SRC, "-o", OPS, "-L" + os.path.join(at, "lib"), "-ltorch_python",
+            "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L" + HERE, "-l:libmoe.so", "-Wl,-rpath,$ORIGIN"]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -64,9 +65,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if force or _stale(obj, [src] + headers):
             jobs.append([NVCC, *ARCH, *FLAGS, "-c", src, "-o", obj] + (["-Xptxas", "-v"] if verbose else []))
 
-    if force or _stale(ARGS, [ARGS_SRC]):
-        jobs.append(_args_command())
-
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
@@ -79,6 +77,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
                 sys.stderr.write(out)
     if force or _stale(LIB, objs):
         subprocess.run([NVCC, *ARCH, "-shared", "-o", LIB, *objs, "-lcudart"], check=True)
+    if force or _stale(OPS, [OPS_SRC, LIB] + headers):
+        run(_ops_command())
     return LIB
 
 

@@ -1,4 +1,5 @@
-"""Thin ctypes binding of ``libmoe.so`` (include/moe.h, moe_cache.h, moe_ops.h).
+"""Thin binding of ``libmoe.so``: ctypes for include/moe.h and moe_cache.h, an
+extension module for moe_ops.h.
 
 Argument marshalling only: every step of the expert pass runs in the CUDA
 library.  Tensors are torch CUDA tensors; their device pointers and the current
@@ -292,162 +293,32 @@ def moe_slot_fill(pool: moe_pool, slot, host_codes, host_scales, stream=None):
                                                 ctypes.c_void_p(host_scales.data_ptr()), _stream(stream)))
 
 
-# The operators of moe_ops.h.  The tensors of a call lie on one device, which
-# need not be the current one; the call goes to `stream` or to that device's
-# current stream.
-_DTYPES = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32}
-_GATE_MODES = {None: 0, "none": 0, "channel": 1, "token": 2}
-_I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
+# The operators of moe_ops.h are bound natively (csrc/binding.cpp, _ops.so; help(moe.moe_permute) and so on shows
+# their arguments).  The tensors of a call lie on one device, which need not be the current one; the call goes to
+# `stream` or to that device's current stream.  Looked up here at their first use.
+_OPS = ("moe_permute", "moe_permute_backward", "moe_unpermute", "moe_unpermute_backward", "moe_route_backward",
+        "moe_block_norm", "moe_block_norm_backward")
 
 
-def _dtype(name, t):
-    if t.dtype not in _DTYPES:
-        raise ValueError(f"{name} must be bfloat16, float16 or float32, not {t.dtype}")
-    return _DTYPES[t.dtype]
-
-
-_device_index = torch.Tensor.get_device
-
-
-def _arg(name, t, dtype, shape, device):
-    """The device address of a contiguous tensor of this type and shape on this device (None for None), or a
-    ValueError.  The first call puts the extension module's function (csrc/args.cpp) in this one's place."""
-    global _arg
+def __getattr__(name):
+    if name not in _OPS:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    lib()
     try:
-        from ._args import address
+        from . import _ops
     except ImportError as e:
-        raise RuntimeError("bit_expert_ffn_route_b200/_args.so is missing or does not fit this torch: run `python -m "
+        raise RuntimeError("bit_expert_ffn_route_b200/_ops.so is missing or does not fit this torch: run `python -m "
                            "bit_expert_ffn_route_b200.build --force`") from e
-    _arg = address
-    return address(name, t, dtype, shape, device)
-
-
-def _call(fn, device, stream, *args):
-    """One call on CUDA device `device` (an index; -1: the tensors are not on one)."""
-    if device < 0:
-        raise ValueError(f"{fn} takes CUDA tensors")
-    if stream is not None and stream.device.index != device:
-        raise ValueError(f"{fn}: the stream is on {stream.device}, the tensors on cuda:{device}")
-    if device != torch._C._cuda_getDevice():
-        with torch.cuda.device(device):
-            return _call(fn, device, stream, *args)
-    # the numbers alone: torch.cuda.current_device() and current_stream() (which makes an object) take 3.5 us
-    handle = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
-    st = getattr(_lib or lib(), fn)(*args, handle)
-    if st != MOE_OK:
-        raise MoeError(fn, st)
-
-
-def moe_permute(ids, E, offsets, pair_row, row_pair, x=None, rows=None, slot_table=None, n_slots=None, stream=None):
-    """Tokens sorted by expert: rows[i] = x[row_pair[i] // k], grouped by expert (all pairs, or with slot_table the
-    missed ones, given n_slots as well).  Without x and rows only the plan (offsets, pair_row, row_pair) is made."""
-    T, k = ids.shape
-    if slot_table is not None and n_slots is None:
-        raise ValueError("moe_permute: slot_table comes with the pool's n_slots")
-    dev = _device_index(ids)
-    dt, D = (MOE_BF16, 1) if x is None else (_dtype("x", x), x.shape[-1])
-    _call("moe_permute", dev, stream, _arg("ids", ids, _I32, (T, k), dev), T, k, E,
-          _arg("slot_table", slot_table, _I32, (E,), dev), n_slots or 0,
-          None if x is None else _arg("x", x, x.dtype, (T, D), dev), D, dt,
-          None if x is None and rows is None else _arg("rows", rows, rows.dtype if x is None else x.dtype, (T * k, D),
-                                                       dev),
-          _arg("offsets", offsets, _I32, (E + 1,), dev), _arg("pair_row", pair_row, _I32, (T, k), dev),
-          _arg("row_pair", row_pair, _I32, (T * k,), dev))
-
-
-def moe_permute_backward(drows, pair_row, dx, stream=None):
-    """dx[t] = the sum of drows over token t's rows."""
-    T, k = pair_row.shape
-    n, D = drows.shape
-    dev = _device_index(drows)
-    _call("moe_permute_backward", dev, stream, _arg("drows", drows, drows.dtype, (n, D), dev), n,
-          _arg("pair_row", pair_row, _I32, (T, k), dev), T, k, D, _dtype("drows", drows),
-          _arg("dx", dx, drows.dtype, (T, D), dev))
-
-
-def moe_unpermute(rows, pair_row, out, weights=None, stream=None):
-    """out[t] = the sum of weights[t, r] * rows[pair_row[t, r]]; out of rows' type or float32 (a miss_partial)."""
-    T, k = pair_row.shape
-    n, D = rows.shape
-    dev = _device_index(rows)
-    _call("moe_unpermute", dev, stream, _arg("rows", rows, rows.dtype, (n, D), dev), n,
-          _arg("pair_row", pair_row, _I32, (T, k), dev), _arg("weights", weights, _F32, (T, k), dev), T, k, D,
-          _dtype("rows", rows), _arg("out", out, out.dtype, (T, D), dev), _dtype("out", out))
-
-
-def moe_unpermute_backward(dout, pair_row, drows=None, rows=None, weights=None, dweights=None, stream=None):
-    """drows[pair_row[t, r]] = weights[t, r] * dout[t] and dweights[t, r] = <dout[t], rows[pair_row[t, r]]>."""
-    T, k = pair_row.shape
-    like = drows if drows is not None else rows
-    if like is None:
-        raise ValueError("moe_unpermute_backward writes drows, dweights (from rows), or both")
-    n, D = like.shape
-    dev = _device_index(dout)
-    _call("moe_unpermute_backward", dev, stream, _arg("dout", dout, dout.dtype, (T, D), dev), _dtype("dout", dout),
-          _arg("rows", rows, like.dtype, (n, D), dev), n, _arg("pair_row", pair_row, _I32, (T, k), dev),
-          _arg("weights", weights, _F32, (T, k), dev), T, k, D, _dtype("rows", like),
-          _arg("drows", drows, like.dtype, (n, D), dev), _arg("dweights", dweights, _F32, (T, k), dev))
+    globals().update({n: getattr(_ops, n) for n in _OPS})
+    return globals()[name]
 
 
 def route_backward_workspace_size(T, D, E, k) -> int:
     return int(lib().moe_route_backward_workspace_size(T, D, E, k))
 
 
-def moe_route_backward(dgates, gates, ids, x, Wr, offsets, row_pair, dlogits, ws, dx=None, dx_add=None, dWr=None,
-                       dbias=None, stream=None):
-    """Gradient of moe_route_topk's gates; offsets and row_pair are moe_permute's of the same ids (no slot_table)."""
-    T, k = ids.shape
-    E, D = Wr.shape
-    dev = _device_index(ids)
-    _call("moe_route_backward", dev, stream, _arg("dgates", dgates, _F32, (T, k), dev),
-          _arg("gates", gates, _F32, (T, k), dev), _arg("ids", ids, _I32, (T, k), dev),
-          _arg("x", x, _BF16, (T, D), dev), _arg("Wr", Wr, _BF16, (E, D), dev),
-          _arg("offsets", offsets, _I32, (E + 1,), dev), _arg("row_pair", row_pair, _I32, (T * k,), dev), T, D, E, k,
-          _arg("dx_add", dx_add, _BF16, (T, D), dev), _arg("dlogits", dlogits, _F32, (T, k), dev),
-          _arg("dx", dx, _BF16, (T, D), dev), _arg("dWr", dWr, _F32, (E, D), dev),
-          _arg("dbias", dbias, _F32, (E,), dev), _arg("ws", ws, torch.uint8, ws.shape, dev), ws.numel())
-
-
-def _gate(gate, gate_mode, T, D):
-    if gate_mode not in _GATE_MODES:
-        raise ValueError(f"gate_mode must be 'none', 'channel' or 'token', not {gate_mode!r}")
-    mode = _GATE_MODES[gate_mode]
-    return mode, (T,) if mode == 2 else (D,)
-
-
-def moe_block_norm(y, x_out=None, residual=None, alpha=1.0, gate=None, gate_mode=None, w_post=None, w_next=None,
-                   normed=None, rstd_post=None, rstd_next=None, eps=1e-6, stream=None):
-    """x_out = alpha * residual + gate * norm(y) * w_post (y itself without w_post); normed = norm(x_out) * w_next.
-    gate_mode: 'channel' (gate [D]) or 'token' (gate [T])."""
-    T, D = y.shape
-    dev, dt = _device_index(y), y.dtype
-    mode, gs = _gate(gate, gate_mode, T, D)
-    _call("moe_block_norm", dev, stream, _arg("y", y, dt, (T, D), dev), _arg("residual", residual, dt, (T, D), dev),
-          _arg("gate", gate, _F32, gs, dev), mode, alpha, _arg("w_post", w_post, _F32, (D,), dev),
-          _arg("w_next", w_next, _F32, (D,), dev), eps, T, D, _dtype("y", y), _arg("x_out", x_out, dt, (T, D), dev),
-          _arg("normed", normed, dt, (T, D), dev), _arg("rstd_post", rstd_post, _F32, (T,), dev),
-          _arg("rstd_next", rstd_next, _F32, (T,), dev))
-
-
 def block_norm_backward_workspace_size(T, D) -> int:
     return int(lib().moe_block_norm_backward_workspace_size(T, D))
-
-
-def moe_block_norm_backward(dx_out, dnormed, x_out, y, dy, ws, dresidual=None, alpha=1.0, gate=None, gate_mode=None,
-                            dgate=None, w_post=None, dw_post=None, rstd_post=None, w_next=None, dw_next=None,
-                            rstd_next=None, stream=None):
-    """Gradients of moe_block_norm; the arguments left None there stay None here, as do gradients not wanted."""
-    T, D = dy.shape
-    dev, dt = _device_index(dy), dy.dtype
-    mode, gs = _gate(gate, gate_mode, T, D)
-    _call("moe_block_norm_backward", dev, stream, _arg("dx_out", dx_out, dt, (T, D), dev),
-          _arg("dnormed", dnormed, dt, (T, D), dev), _arg("x_out", x_out, dt, (T, D), dev),
-          _arg("y", y, dt, (T, D), dev), _arg("gate", gate, _F32, gs, dev), mode, alpha,
-          _arg("w_post", w_post, _F32, (D,), dev), _arg("rstd_post", rstd_post, _F32, (T,), dev),
-          _arg("w_next", w_next, _F32, (D,), dev), _arg("rstd_next", rstd_next, _F32, (T,), dev), T, D,
-          _dtype("dy", dy), _arg("dy", dy, dt, (T, D), dev), _arg("dresidual", dresidual, dt, (T, D), dev),
-          _arg("dgate", dgate, _F32, gs, dev), _arg("dw_post", dw_post, _F32, (D,), dev),
-          _arg("dw_next", dw_next, _F32, (D,), dev), _arg("ws", ws, torch.uint8, ws.shape, dev), ws.numel())
 
 
 class Layer:

@@ -162,3 +162,36 @@ def test_binding_refuses_tensors_it_cannot_pass(L):
         moe.moe_block_norm(x, x, gate=torch.zeros(8), gate_mode="row")
     with pytest.raises(ValueError, match="gate "):
         moe.moe_block_norm(x, torch.zeros(4, 8), gate=torch.zeros(8), gate_mode="token")
+
+
+def test_binding_takes_its_arguments_as_python_does(L):
+    """By position and by name; a missing, unknown, doubled or surplus one is a TypeError, a number that does not
+    fit a ValueError (CPU tensors again)."""
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)     # noqa: E731
+    ids, plan = i32(4, 2), (i32(6), i32(4, 2), i32(8))
+    y, xo = torch.zeros(4, 8), torch.zeros(4, 8)
+    for call in (lambda: moe.moe_permute(ids, 5, *plan), lambda: moe.moe_permute(ids, E=5, row_pair=plan[2],
+                                                                                pair_row=plan[1], offsets=plan[0]),
+                 lambda: moe.moe_block_norm(y, xo, None, 0.5), lambda: moe.moe_block_norm(y, x_out=xo, alpha=1)):
+        with pytest.raises(ValueError, match="CUDA"):       # every argument was accepted
+            call()
+    with pytest.raises(TypeError, match="needs row_pair"):
+        moe.moe_permute(ids, 5, *plan[:2])
+    with pytest.raises(TypeError, match="no parameter 'rowpair'"):
+        moe.moe_permute(ids, 5, *plan[:2], rowpair=plan[2])
+    with pytest.raises(TypeError, match="two values for E"):
+        moe.moe_permute(ids, 5, *plan, E=5)
+    with pytest.raises(TypeError, match="at most 4"):
+        moe.moe_permute_backward(y, ids, xo, None, None)
+    with pytest.raises(TypeError):
+        moe.moe_block_norm(y, xo, alpha="1")
+    with pytest.raises(TypeError):
+        moe.moe_permute(ids, 5.0, *plan)
+    with pytest.raises(ValueError, match="E is out of range"):
+        moe.moe_permute(ids, 1 << 40, *plan)
+    with pytest.raises(ValueError, match="two dimensions"):
+        moe.moe_permute(ids.view(-1), 5, *plan)
+    with pytest.raises(ValueError, match="ids must be a tensor"):
+        moe.moe_permute([[0]], 5, *plan)
+    with pytest.raises(AttributeError):
+        moe.moe_unsorted
