@@ -7,7 +7,7 @@
 // likewise: four rows in, two out.  HBM is the floor of both; what bounds them is
 // the chain of a token's steps (rows out of shared memory, a sum over the block's
 // warps, the rest) with as many warps as the registers leave.  4,096 tokens of
-// 3,072 bf16: 20 us forward (100 MB, 5.1 TB/s) and 38 us backward (151 MB, 4.0
+// 3,072 bf16: 20 us forward (100 MB, 5.1 TB/s) and 36 us backward (151 MB, 4.2
 // TB/s; 31 us of it the tokens, the rest the join of the partial sums).
 //
 // Threads: a group of whole warps takes a token, each thread the same columns of
@@ -18,7 +18,7 @@
 // Rows of whole 16-byte packs: a thread copies just what it will read itself, so
 // no barrier guards the copies.  Other rows start anywhere: the 16-byte blocks
 // that cover the row are copied (elements where such a block reaches over the
-// buffer's ends), and read back an element at a time behind a barrier.
+// buffer's ends), and read back an element at a time, or a pair, behind a barrier.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -29,11 +29,12 @@
 namespace moe {
 namespace {
 
-constexpr int kNormParts = 296;        // most blocks of the backward pass, two per SM: each leaves a partial of every
+constexpr int kNormParts = 148;        // most blocks of the backward pass, one per SM: each leaves a partial of every
                                        // sum over tokens
-constexpr int kJoinEach = kNormParts / 8;   // of which a warp of the join adds up so many
+constexpr int kJoinEach = (kNormParts + 7) / 8;     // of which a warp of the join adds up so many
 constexpr int kNormThreads = 384;      // threads that the groups of a block fill, about
-constexpr int kMaxGroups = 12;         // named barriers 1..12
+constexpr int kGradThreads = 768;      // and of the backward pass: one block per SM, half the partials of blocks of
+                                       // 384, and three tokens where D is 2,048 (59 us, with 384 71 us, of 12,288 bf16)
 constexpr int kMaxDynamic = 227 * 1024;
 
 template <int N>
@@ -143,17 +144,22 @@ struct Group {
 };
 constexpr int kSumFloats = 256;
 
-// How rows lie: they start anywhere (ANY), they are of whole 16-byte packs
-// (WIDE), or besides every thread of the group has all its columns and the call
-// has every operand but a token gate (FULL: no test of these in the token's path;
-// 4,096 x 3,072 bf16 forward 19.2 us against 21.3 us, backward 38 against 40).
-enum { ANY, WIDE, FULL };
+// How rows lie: they start anywhere (ANY), they are of whole PAIRS of 16-bit
+// elements (13,519 x 2,482 fp16 forward 73 us, 92 us as single elements; 6,000 x
+// 6,002 bf16 backward 147 against 221) or of whole 16-byte packs (WIDE), or besides
+// every thread of the group has all its columns and the call has every operand but
+// a token gate (FULL: no test of these in the token's path; 4,096 x 3,072 bf16
+// forward 19.2 us against 21.3 us, backward 38 against 40).
+enum { ANY, PAIRS, WIDE, FULL };
 
 // Thread `rank` of a group of `size` owns N elements of a row: packs of V, at
 // (i size + rank) V (V = 1: single elements of rows that start anywhere).
 template <typename T, int N, int KIND>
 struct Cols {
-    static constexpr int V = KIND != ANY ? (N < 16 / (int)sizeof(T) ? N : 16 / (int)sizeof(T)) : 1, ITER = N / V;
+    static constexpr int V = KIND == ANY     ? 1
+                             : KIND == PAIRS ? 2
+                             : N < 16 / (int)sizeof(T) ? N : 16 / (int)sizeof(T),
+                         ITER = N / V;
     int rank, size, D;
     MOE_DEVINL int at(int i) const { return (i * size + rank) * V; }
     MOE_DEVINL bool in(int i) const { return KIND == FULL || at(i) < D; }
@@ -193,7 +199,7 @@ struct Ring {
     int slot = 0;                               // offset in the ring of the token to read next, then to fetch into
     // bytes from the row's place in its slot to its first element
     MOE_DEVINL int lead(int r, uint32_t at) const {
-        return KIND != ANY ? 0 : (int)((uintptr_t)(static_cast<const char*>(a.rows[r]) + at) & 15);
+        return KIND >= WIDE ? 0 : (int)(((uint32_t)(uintptr_t)a.rows[r] + at) & 15);
     }
     // Fetch the token at offset `at`, if there is one.
     MOE_DEVINL void fetch(uint32_t at, bool live) {
@@ -203,7 +209,7 @@ struct Ring {
                 if (KIND != FULL && !a.rows[r]) continue;
                 const char* src = static_cast<const char*>(a.rows[r]);
                 char* to = ring + slot + r * a.pitch;
-                if constexpr (KIND != ANY) {
+                if constexpr (KIND >= WIDE) {
 #pragma unroll
                     for (int i = 0; i < Cols<T, N, KIND>::ITER; ++i)
                         if (col.in(i))
@@ -230,7 +236,7 @@ struct Ring {
     }
     MOE_DEVINL void wait(const Group& grp) const {
         cp_async_wait<STAGES - 1>();
-        if (KIND == ANY) grp.sync();
+        if (KIND < WIDE) grp.sync();
     }
     MOE_DEVINL void read(int r, uint32_t at, float (&v)[N]) const {
         col.load(reinterpret_cast<const T*>(ring + slot + r * a.pitch + lead(r, at)), v);
@@ -359,10 +365,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 3 : 1)
             mul(v, v, w);
             mul(v, v, rx);
             col.store(at_bytes<T>(a.normed, at), v);
-        } else if (KIND == ANY) {
+        } else if (KIND < WIDE) {
             grp.sync();                         // all of the group have read the token
         }
-        if (KIND == ANY && a.group == 32) __syncwarp();     // the sums above had no barrier
+        if (KIND < WIDE && a.group == 32) __syncwarp();     // the sums above had no barrier
         in.fetch(at + STAGES * skip, t + STAGES * step < a.T);
         at += skip;
     }
@@ -389,7 +395,7 @@ struct NormGradArgs {
 //   SMEM: the sums over tokens are kept in shared memory, for rows too wide for
 //   the registers.
 template <typename T, int N, int STAGES, int THREADS, bool SMEM, int KIND>
-__global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 2 : 1)
+__global__ void __launch_bounds__(THREADS)
     block_norm_backward_kernel(const __grid_constant__ NormGradArgs a) {
     extern __shared__ __align__(16) float dyn[];        // the groups' sums, [2][D] over tokens, the factors, the rings
     const int groups = blockDim.x / a.group, g = threadIdx.x / a.group, rank = threadIdx.x % a.group;
@@ -397,8 +403,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 2 : 1)
     Group grp{g, rank, a.group, dyn + g * kSumFloats};
     const Cols<T, N, KIND> col{rank, a.group, a.D};
     constexpr bool KEPT = kept_factors<T>(SMEM);
-    float* sums = dyn + groups * kSumFloats;            // with SMEM or several groups
-    const int sums_floats = SMEM || groups > 1 ? (2 * a.D + 3) / 4 * 4 : 0;
+    float* sums = dyn + groups * kSumFloats;
+    const int sums_floats = SMEM ? (2 * a.D + 3) / 4 * 4 : 0;
     char* rings = reinterpret_cast<char*>(sums + sums_floats + (KEPT ? 0 : 2 * N * a.group));
     Ring<T, N, 4, STAGES, KIND, NormGradArgs> in{a, col, rings + g * STAGES * 4 * a.pitch};
     const uint32_t skip = step * a.D * (uint32_t)sizeof(T);
@@ -466,7 +472,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 2 : 1)
             s2 = dot(m, xh);
         }
         grp.sum3(s0, s1, s2);
-        if (KIND == ANY && a.group == 32) __syncwarp();     // the sums had no barrier
+        if (KIND < WIDE && a.group == 32) __syncwarp();     // the sums had no barrier
         in.fetch(at + STAGES * skip, t + STAGES * step < a.T);  // all of the group have read the token
         const float rc1 = rx * s0 * inv, sq = __fmaf_rn(-rc1, s2, s1);
         const float c2 = post ? gt * sq * inv : 0.f;
@@ -491,28 +497,26 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 2 : 1)
         col.store(at_bytes<T>(a.dy, at), b);
         at += skip;
     }
-    // The block's sums: from the registers, or those of its groups added in order.
+    // The block's sums: those of its groups added in order.
     float* part = a.part + (size_t)blockIdx.x * 2 * a.D;
     if constexpr (SMEM) {
         __syncthreads();
         for (int i = threadIdx.x; i < 2 * a.D; i += blockDim.x) part[i] = sums[i];
+    } else if (groups == 1) {
+        if (a.want_next) col.store(part, s_next);
+        if (a.want_post) col.store(part + a.D, s_gy);
     } else {
-        for (int i = 0; i < groups; ++i) {
-            if (i == g) {
-                float w[N];
-                float* to = i == groups - 1 ? part : sums;
-                if (i > 0) {
-                    col.load(sums, w);
-#pragma unroll
-                    for (int j = 0; j < N; ++j) s_next[j] += w[j];
-                    col.load(sums + a.D, w);
-#pragma unroll
-                    for (int j = 0; j < N; ++j) s_gy[j] += w[j];
-                }
-                if (a.want_next) col.store(to, s_next);
-                if (a.want_post) col.store(to + a.D, s_gy);
-            }
-            if (groups > 1) __syncthreads();
+        const int pitch = STAGES * 4 * a.pitch / 4;     // floats from ring to ring: 2 D and more
+        __syncthreads();                        // the rings are read out
+        float* mine = reinterpret_cast<float*>(rings) + g * pitch;
+        if (a.want_next) col.store(mine, s_next);
+        if (a.want_post) col.store(mine + a.D, s_gy);
+        __syncthreads();
+        for (int i = threadIdx.x; i < 2 * a.D; i += blockDim.x) {
+            if (!(i < a.D ? a.want_next : a.want_post)) continue;
+            float v = 0.f;
+            for (int q = 0; q < groups; ++q) v += reinterpret_cast<const float*>(rings)[q * pitch + i];
+            part[i] = v;
         }
     }
 }
@@ -550,10 +554,9 @@ __global__ void __launch_bounds__(256) block_norm_join_kernel(const float* __res
 // Threads per token, tokens per block and bytes of a row's slot.
 struct NormShape {
     int group, groups, pitch;
-    NormShape(int D, int per_thread, size_t elem, bool wide) {
+    NormShape(int D, int per_thread, size_t elem, bool wide, int threads) {
         group = ((D + per_thread - 1) / per_thread + 31) / 32 * 32;
-        groups = group >= kNormThreads ? 1 : kNormThreads / group;
-        if (groups > kMaxGroups) groups = kMaxGroups;
+        groups = group >= threads ? 1 : threads / group;
         pitch = (int)((D * elem + 15) / 16 * 16) + (wide ? 0 : 16);
     }
     int blocks(int T, int most) const {
@@ -565,7 +568,7 @@ struct NormShape {
 template <typename T, int N, int STAGES, int THREADS, int KIND>
 cudaError_t run_norm(NormArgs a, cudaStream_t s) {
     auto kernel = block_norm_kernel<T, N, STAGES, THREADS, KIND>;
-    const NormShape n(a.D, N, sizeof(T), KIND != ANY);
+    const NormShape n(a.D, N, sizeof(T), KIND >= WIDE, kNormThreads);
     static std::atomic<uint64_t> set{0};
     if (!once_per_device(set, [&] {
             return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic) ==
@@ -581,7 +584,7 @@ cudaError_t run_norm(NormArgs a, cudaStream_t s) {
 template <typename T, int N, int STAGES, int THREADS, bool SMEM, int KIND>
 cudaError_t run_norm_backward(NormGradArgs a, int* blocks, cudaStream_t s) {
     auto kernel = block_norm_backward_kernel<T, N, STAGES, THREADS, SMEM, KIND>;
-    const NormShape n(a.D, N, sizeof(T), KIND != ANY);
+    const NormShape n(a.D, N, sizeof(T), KIND >= WIDE, THREADS);
     static std::atomic<uint64_t> set{0};
     if (!once_per_device(set, [&] {
             return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic) ==
@@ -590,17 +593,17 @@ cudaError_t run_norm_backward(NormGradArgs a, int* blocks, cudaStream_t s) {
         return cudaErrorUnknown;
     a.group = n.group;
     a.pitch = n.pitch;
-    const int sms = device_sm_count() < kNormParts / 2 ? device_sm_count() : kNormParts / 2;
-    *blocks = n.blocks(a.T, THREADS == kNormThreads ? 2 * sms : sms);
-    const size_t sums = SMEM || n.groups > 1 ? (size_t)(2 * a.D + 3) / 4 * 16 : 0;
+    *blocks = n.blocks(a.T, device_sm_count() < kNormParts ? device_sm_count() : kNormParts);
+    const size_t sums = SMEM ? (size_t)(2 * a.D + 3) / 4 * 16 : 0;
     const size_t factors = kept_factors<T>(SMEM) ? 0 : (size_t)n.group * N * 8;
     return launch_pdl(kernel, dim3(*blocks), dim3(n.group * n.groups),
                       sums + factors + (size_t)n.groups * (kSumFloats * 4 + STAGES * 4 * n.pitch), s, a);
 }
 
-// A thread has 16 bytes of a row (twice that for fp32 rows beyond 4,096).  Blocks
-// of 384 threads leave room for two per SM with the sums over tokens in
-// registers; beyond 4,096 elements those go to shared memory.
+// A thread has 16 bytes of a row (twice that for fp32 rows beyond 4,096).  Forward
+// blocks of 384 threads leave room for three per SM; 768 threads of the backward
+// pass, two tokens or more, for the sums over tokens in registers.  Beyond 4,096
+// elements those go to shared memory.
 template <typename T, int KIND>
 cudaError_t pick_norm(const NormArgs& a, cudaStream_t s) {
     constexpr int N = 16 / sizeof(T);
@@ -614,7 +617,7 @@ cudaError_t pick_norm(const NormArgs& a, cudaStream_t s) {
 template <typename T, int KIND>
 cudaError_t pick_norm_backward(const NormGradArgs& a, int* blocks, cudaStream_t s) {
     constexpr int N = 16 / sizeof(T);
-    if (a.D <= kNormThreads * N) return run_norm_backward<T, N, 3, kNormThreads, false, KIND>(a, blocks, s);
+    if (a.D <= kGradThreads / 2 * N) return run_norm_backward<T, N, 3, kGradThreads, false, KIND>(a, blocks, s);
     if (a.D <= 512 * N) return run_norm_backward<T, N, 3, 512, false, KIND>(a, blocks, s);
     if constexpr (N == 8) {
         return run_norm_backward<T, N, 1, 1024, true, KIND>(a, blocks, s);
@@ -660,9 +663,13 @@ extern "C" moe_status moe_block_norm(const void* y, const void* residual, const 
     if (!ops_aligned(y, es) || !ops_aligned(residual, es) || !ops_aligned(x_out, es) || !ops_aligned(normed, es) ||
         !ops_aligned(w_post, 4) || !ops_aligned(w_next, 4) || !ops_aligned(rstd_post, 4) || !ops_aligned(rstd_next, 4))
         return MOE_ERR_INVALID_ARG;
-    const bool wide = (D * es) % 16 == 0 && ops_aligned(y, 16) && ops_aligned(residual, 16) && ops_aligned(x_out, 16) &&
-                      ops_aligned(normed, 16) && ops_aligned(w_post, 16) && ops_aligned(w_next, 16) &&
-                      (gate_mode != MOE_GATE_CHANNEL || ops_aligned(gate, 16));
+    // rows of whole units of n bytes, in buffers that start with one; fp32 arrays likewise
+    auto units = [&](size_t n, size_t fp32) {
+        return (D * es) % n == 0 && ops_aligned(y, n) && ops_aligned(residual, n) && ops_aligned(x_out, n) &&
+               ops_aligned(normed, n) && ops_aligned(w_post, fp32) && ops_aligned(w_next, fp32) &&
+               (gate_mode != MOE_GATE_CHANNEL || ops_aligned(gate, fp32));
+    };
+    const bool wide = units(16, 16), pairs = units(4, 8);
     const bool full =
         wide && whole_groups(D, es) && residual && w_post && w_next && x_out && gate_mode != MOE_GATE_TOKEN;
     const NormArgs a{{y, residual}, gate, gate_mode, alpha, w_post, w_next,   eps,
@@ -670,6 +677,8 @@ extern "C" moe_status moe_block_norm(const void* y, const void* residual, const 
     cudaStream_t s = (cudaStream_t)stream;
     return with_dtype(dtype, [&](auto e) {
         using Tp = decltype(e);
+        if constexpr (sizeof(Tp) == 2)
+            if (!wide && pairs) return ops_status(pick_norm<Tp, PAIRS>(a, s));
         return ops_status(full   ? pick_norm<Tp, FULL>(a, s)
                           : wide ? pick_norm<Tp, WIDE>(a, s)
                                  : pick_norm<Tp, ANY>(a, s));
@@ -712,10 +721,12 @@ extern "C" moe_status moe_block_norm_backward(const void* dx_out, const void* dn
         !ops_aligned(rstd_post, 4) || !ops_aligned(rstd_next, 4) || !ws || !ops_aligned(ws, 256))
         return MOE_ERR_INVALID_ARG;
     if (ws_bytes < norm_ws_bytes(T, D)) return MOE_ERR_WORKSPACE;
-    const bool wide = (D * es) % 16 == 0 && ops_aligned(dx_out, 16) && ops_aligned(dnormed, 16) &&
-                      ops_aligned(x_out, 16) && ops_aligned(y, 16) && ops_aligned(dy, 16) &&
-                      ops_aligned(dresidual, 16) && ops_aligned(w_post, 16) && ops_aligned(w_next, 16) &&
-                      (gate_mode != MOE_GATE_CHANNEL || ops_aligned(gate, 16));
+    auto units = [&](size_t n, size_t fp32) {   // as in the forward pass
+        return (D * es) % n == 0 && ops_aligned(dx_out, n) && ops_aligned(dnormed, n) && ops_aligned(x_out, n) &&
+               ops_aligned(y, n) && ops_aligned(dy, n) && ops_aligned(dresidual, n) && ops_aligned(w_post, fp32) &&
+               ops_aligned(w_next, fp32) && (gate_mode != MOE_GATE_CHANNEL || ops_aligned(gate, fp32));
+    };
+    const bool wide = units(16, 16), pairs = units(4, 8);
     const bool per_token = gate_mode == MOE_GATE_TOKEN;
     const bool full = wide && whole_groups(D, es) && dx_out && w_post && w_next && dresidual && !per_token;
     const NormGradArgs a{{w_next ? x_out : nullptr, w_next ? dnormed : nullptr, dx_out, w_post || dgate ? y : nullptr},
@@ -725,6 +736,8 @@ extern "C" moe_status moe_block_norm_backward(const void* dx_out, const void* dn
     int blocks = 0;
     st = with_dtype(dtype, [&](auto e) {
         using Tp = decltype(e);
+        if constexpr (sizeof(Tp) == 2)
+            if (!wide && pairs) return ops_status(pick_norm_backward<Tp, PAIRS>(a, &blocks, s));
         return ops_status(full   ? pick_norm_backward<Tp, FULL>(a, &blocks, s)
                           : wide ? pick_norm_backward<Tp, WIDE>(a, &blocks, s)
                                  : pick_norm_backward<Tp, ANY>(a, &blocks, s));

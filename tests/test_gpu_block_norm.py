@@ -31,6 +31,12 @@ CASES = [
     (1000, 64, BF, "channel", False, True, True, 1.0, 1),
     (2100, 136, FL, "channel", True, True, True, 1.0, 0),
     (33, 2048, FL, "none", True, False, False, 1.0, 1),
+    (701, 322, HF, "token", True, True, True, 0.25, 0),     # rows of pairs
+    (301, 1026, BF, "channel", True, True, True, 1.0, 2),
+    (150, 2048, BF, "none", True, True, True, 1.0, 2),
+    (5, 6002, HF, "channel", True, False, True, 1.414, 0),
+    (7300, 18, BF, "token", True, True, True, 1.0, 0),      # 24 tokens in a block
+    (7300, 24, BF, "channel", True, True, True, 1.0, 0),
 ]
 NAMES = [f"T{c[0]}D{c[1]}{c[3]}{int(c[4])}{int(c[5])}{int(c[6])}" for c in CASES]
 
