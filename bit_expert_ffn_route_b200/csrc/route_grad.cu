@@ -5,17 +5,19 @@
 //   dWr[e] = sum over the pairs of e of dl x[t],  dbias[e] = sum of dl
 //
 // Only k of E logits of a token have a gradient, so both products run over the
-// pairs (2 P D multiply-adds in fp32) and not over all experts: as dense products
-// on the tensor cores they would be 51 times the work at 512 experts and 10 per
-// token, three times over for dl in three bf16 terms.  HBM sees little (x, Wr, dx,
-// dWr once each); what bounds the two is reading a row of x or Wr per pair, 251 MB
-// each at 40,960 pairs of 3,072, out of L2 or shared memory, with its unpacking.
+// pairs (2 P D multiply-adds in fp32) and not over all experts, unless these are few
+// (route_dense.cuh): as dense products on the tensor cores they would be 51 times the
+// work at 512 experts and 10 per token, three times over for dl in three bf16 terms.
+// HBM sees little (x, Wr, dx, dWr once each); what bounds the two is reading a row of
+// x or Wr per pair, 251 MB each at 40,960 pairs of 3,072, out of L2 or shared memory,
+// with its unpacking.
 // 4,096 tokens, 512 experts, 10 x 3,072: 55 us in all (logits 3, dx 23, dWr 28,
 // join 7, overlapping at their ends).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "once.cuh"
+#include "route_dense.cuh"
 #include "rows.cuh"
 #include "sync.cuh"
 
@@ -34,6 +36,7 @@ constexpr int kDwSmallT = 32;              // tokens whose experts' rows are sum
 constexpr int kDwMaxChunk = 3328;          // rows whose places fit in 40 KB of shared memory
 constexpr int kDwSums = 320 * 3072;        // partial sums that the dWr chunks make, about
 constexpr int kDwDepth = 4;                // rows of x in flight per thread
+constexpr int kDenseMinT = 16;             // tokens from which on few experts go to the tensor cores
 constexpr int kJoinThreads = 256;
 constexpr int kJoinParts = 4;              // shares of an expert's partial sums, added up at the same time
 constexpr int kJoinCols = kJoinThreads / kJoinParts * 8;
@@ -405,7 +408,15 @@ moe_status route_grad_shapes(int T, int D, int E, int k) {
     return MOE_OK;
 }
 
-size_t route_grad_ws_bytes(int T, int D, int k) {
+// Few experts, or few more of which a token takes five and more: dense products.
+// Whole calls, dense against pair by pair: 8,266 x 16 of 19 x 256 13 us and 29 us,
+// 20,000 x 2 of 8 x 1,024 26 and 46, 32 x 8 of 16 x 2,048 5.5 and 9.9, 4 tokens 5.9
+// and 5.8; of 32 experts, 1,024 x 4,096, 6 per token 14.9 and 16.0, 4 per token 14.7
+// and 13.0; of 64 (an experts' tile twice as wide) 4,096 x 8 x 2,048 38 and 34.
+bool route_dense(int T, int E, int k) { return T >= kDenseMinT && (E <= 16 || (E <= kDenseMaxE && k >= 5)); }
+
+size_t route_grad_ws_bytes(int T, int D, int E, int k) {
+    if (route_dense(T, E, k)) return 256 + dense_part_bytes(T, D, E);
     const int P = T * k, chunk = P ? dw_chunk(P, D) : 16;
     return 256 + (size_t)2 * ((P + chunk - 1) / chunk) * D * 4;
 }
@@ -470,7 +481,7 @@ cudaError_t launch_dx(const float* dgates, const float* gates, const int32_t* id
 using namespace moe;
 
 extern "C" size_t moe_route_backward_workspace_size(int T, int D, int E, int k) {
-    return route_grad_shapes(T, D, E, k) == MOE_OK ? route_grad_ws_bytes(T, D, k) : 0;
+    return route_grad_shapes(T, D, E, k) == MOE_OK ? route_grad_ws_bytes(T, D, E, k) : 0;
 }
 
 extern "C" moe_status moe_route_backward(const float* dgates, const float* gates, const int32_t* ids,
@@ -496,8 +507,14 @@ extern "C" moe_status moe_route_backward(const float* dgates, const float* gates
     if ((dx && !Wr) || (dx_add && !dx) || (dWr && !x) || ((dWr || dbias) && (!offsets || !row_pair)))
         return MOE_ERR_INVALID_ARG;
     if (dx && (dx == x || dx == Wr)) return MOE_ERR_INVALID_ARG;
-    if (ws_bytes < route_grad_ws_bytes(T, D, k)) return MOE_ERR_WORKSPACE;
+    if (ws_bytes < route_grad_ws_bytes(T, D, E, k)) return MOE_ERR_WORKSPACE;
     const B16 *xb = reinterpret_cast<const B16*>(x), *Wb = reinterpret_cast<const B16*>(Wr);
+    if (route_dense(T, E, k)) {
+        const DenseArgs a{dgates, gates, ids, dWr ? xb : nullptr, Wb, T, D, E, k, dense_chunk(T, D, E),
+                          reinterpret_cast<const B16*>(dx_add), dlogits, reinterpret_cast<B16*>(dx), static_cast<float*>(ws)};
+        return ops_status(E <= 16   ? run_route_dense<16>(a, dWr, dbias, s)
+                                    : run_route_dense<32>(a, dWr, dbias, s));
+    }
     cudaError_t e = launch_dx(dgates, gates, ids, Wb, T, D, E, k, reinterpret_cast<const B16*>(dx_add), dlogits,
                               reinterpret_cast<B16*>(dx), s);
     if (e != cudaSuccess || (!dWr && !dbias)) return ops_status(e);

@@ -38,7 +38,11 @@ def call(ids, gates, dg, x, Wr, add=None, **none):
 
 CASES = [(1, 1, 1, 256, "distinct"), (1, 10, 512, 256, "distinct"), (4, 2, 16, 768, "distinct"),
          (33, 16, 16, 256, "distinct"), (70, 3, 9, 512, "wild"), (200, 2, 5, 256, "one"), (40, 4, 8, 256, "none"),
-         (531, 10, 64, 2304, "distinct"), (1300, 2, 3, 256, "wild"), (5, 8, 1024, 8192, "distinct")]
+         (531, 10, 64, 2304, "distinct"), (1300, 2, 3, 256, "wild"), (5, 8, 1024, 8192, "distinct"),
+         # few experts and many tokens: whole tiles and not, every width of the experts' tile, more blocks than one wave
+         (256, 2, 8, 512, "distinct"), (257, 16, 32, 1024, "wild"), (4100, 4, 17, 256, "one"), (700, 6, 64, 256, "none"),
+         (600, 5, 33, 512, "wild"), (9601, 16, 16, 256, "distinct"), (300, 8, 65, 256, "distinct"),
+         (4100, 6, 17, 256, "one"), (600, 5, 31, 768, "wild"), (16, 1, 1, 256, "distinct"), (90, 5, 32, 4096, "none")]
 
 
 @pytest.mark.parametrize("with_add", [False, True])
@@ -60,6 +64,30 @@ def test_against_the_formula(T, k, E, D, kind, with_add):
     assert torch.equal(only["dWr"], got["dWr"])
     only = call(ids, gates, dg, x, Wr, dx=None, dWr=None)
     assert torch.equal(only["dbias"], got["dbias"]) and torch.equal(only["dlogits"], got["dlogits"])
+
+
+@pytest.mark.parametrize("T,E", [(15, 40), (20, 20), (900, 20), (900, 16), (900, 100), (8000, 20), (8000, 8)])
+def test_what_is_not_finite_stays_with_its_pairs(T, E):
+    """An infinity or NaN in x reaches the gradients of that token's experts alone, one in Wr the tokens of that
+    expert, one in dgates that token and its experts."""
+    k, D = 6, 512
+    ids, gates, dg, x, Wr, _ = make(T, k, E, D, "distinct", seed=3)
+    clean = call(ids, gates, dg, x, Wr)
+    x[3, 17], x[7, 300], Wr[5, 40], dg[11, 1] = float("inf"), float("nan"), float("nan"), float("inf")
+    got = call(ids, gates, dg, x, Wr)
+    bad_W, bad_x = torch.zeros(E, D, dtype=torch.bool, device="cuda"), torch.zeros(T, D, dtype=torch.bool, device="cuda")
+    bad_W[ids[3].long(), 17] = bad_W[ids[7].long(), 300] = True
+    bad_W[ids[11].long()] = True
+    bad_x[(ids == 5).any(1), 40] = True
+    bad_x[11] = True
+    assert torch.equal(~got["dWr"].isfinite(), bad_W) and torch.equal(~got["dx"].isfinite(), bad_x)
+    # what they do not reach is right: the same sums in another order, or the same bits
+    want = ref.route_backward(f64(dg).clip(-1e30, 1e30) * (f64(dg) < 1e30), f64(gates), ids.cpu().numpy(),
+                              np.nan_to_num(f64(x), posinf=0, neginf=0), np.nan_to_num(f64(Wr)))
+    assert torch.equal(got["dlogits"][:11], clean["dlogits"][:11])
+    for name, bad, (v, e), dt in (("dx", bad_x, want[1], BF), ("dWr", bad_W, want[2], FL)):
+        ok = (~bad).cpu().numpy()
+        check(got[name][~bad], v[ok], stored(v, e, dt)[ok], name)
 
 
 def test_no_tokens():
