@@ -11,8 +11,8 @@
 // HBM sees little (x, Wr, dx, dWr once each); what bounds the two is reading a row of
 // x or Wr per pair, 251 MB each at 40,960 pairs of 3,072, out of L2 or shared memory,
 // with its unpacking.
-// 4,096 tokens, 512 experts, 10 x 3,072: 55 us in all (logits 3, dx 23, dWr 28,
-// join 7, overlapping at their ends).
+// 4,096 tokens, 512 experts, 10 x 3,072: 54 us in all (logits 3, dx 23, dWr 28,
+// join 6, overlapping at their ends).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -38,8 +38,7 @@ constexpr int kDwSums = 320 * 3072;        // partial sums that the dWr chunks m
 constexpr int kDwDepth = 4;                // rows of x in flight per thread
 constexpr int kDenseMinT = 16;             // tokens from which on few experts go to the tensor cores
 constexpr int kJoinThreads = 256;
-constexpr int kJoinParts = 4;              // shares of an expert's partial sums, added up at the same time
-constexpr int kJoinCols = kJoinThreads / kJoinParts * 8;
+constexpr int kJoinFew = 8;                // chunks per expert, on average, from which on 16 shares join them, not 4
 
 // Eight fp32 sums as four pairs: fma.rn.f32x2 makes two multiply-adds, each
 // rounded as fmaf rounds it.
@@ -265,15 +264,18 @@ __global__ void __launch_bounds__(kDwThreads) route_dw_small_kernel(const float*
 // over its rows and stores the sum at each change of expert: into dWr where all
 // of the expert's rows are in the chunk, otherwise into part[2 chunk] (the
 // expert began before the chunk) or part[2 chunk + 1] (it goes on after it).
-// The next kernel adds those up in chunk order.  A block per expert instead, over
+// The next kernel adds those up in chunk order.  The sums of dl alone go the same
+// way, from the first columns' blocks (SUMS false: only these).  A block per expert instead, over
 // all its rows, took 1,146 us of the same 40,960 pairs: the largest expert's load.
+template <bool SUMS>
 __global__ void __launch_bounds__(kDwThreads) route_dw_kernel(const float* __restrict__ dlogits,
                                                               const int32_t* __restrict__ ids,
                                                               const B16* __restrict__ x,
                                                               const int32_t* __restrict__ offsets,
                                                               const int32_t* __restrict__ row_pair, int P, int D, int E,
                                                               int k, int chunk, float* __restrict__ dWr,
-                                                              float* __restrict__ part) {
+                                                              float* __restrict__ part, float* __restrict__ dbias,
+                                                              float* __restrict__ bias_part) {
     // of every row: the offset of its token in x, with bit 0 set where an expert begins, and dl
     extern __shared__ uint2 s_row[];
     int* s_exp = reinterpret_cast<int*>(s_row + chunk);
@@ -300,15 +302,19 @@ __global__ void __launch_bounds__(kDwThreads) route_dw_kernel(const float* __res
     const int c = (blockIdx.y * blockDim.x + threadIdx.x) * 8;
     if (c >= D) return;
     Sum8 sum;
+    const bool first = blockIdx.y == 0 && dbias;
+    float b = 0.f;
     auto flush = [&](int e) {
         float acc[8];
         sum.get(acc);
         sum = Sum8();
+        const float bias = b;
+        b = 0.f;
         if (e < 0) return;
-        float* to = dWr + (size_t)e * D;
-        if (__ldg(offsets + e) < j0) to = part + (size_t)(2 * blockIdx.x) * D;
-        else if (__ldg(offsets + e + 1) > j0 + n) to = part + (size_t)(2 * blockIdx.x + 1) * D;
-        store_f32<float, 8>(to + c, acc);
+        const bool before = __ldg(offsets + e) < j0, behind = !before && __ldg(offsets + e + 1) > j0 + n;
+        const int slot = 2 * blockIdx.x + behind;
+        if (SUMS) store_f32<float, 8>((before || behind ? part + (size_t)slot * D : dWr + (size_t)e * D) + c, acc);
+        if (first && c == 0) *(before || behind ? bias_part + slot : dbias + e) = bias;
     };
     const B16* xc = x + c;
     int j = 0;
@@ -318,43 +324,46 @@ __global__ void __launch_bounds__(kDwThreads) route_dw_kernel(const float* __res
 #pragma unroll
         for (int i = 0; i < kDwDepth; ++i) {
             row[i] = s_row[j + i];
-            a[i] = load_pack<B16, 8>(xc + (row[i].x & ~1u));
+            if (SUMS) a[i] = load_pack<B16, 8>(xc + (row[i].x & ~1u));
         }
 #pragma unroll
         for (int i = 0; i < kDwDepth; ++i) {
             if (row[i].x & 1u) flush(s_exp[j + i - 1]);
-            sum.add(__uint_as_float(row[i].y), a[i]);
+            if (first) b += __uint_as_float(row[i].y);
+            if (SUMS) sum.add(__uint_as_float(row[i].y), a[i]);
         }
     }
     for (; j < n; ++j) {
         const uint2 row = s_row[j];
         if (row.x & 1u) flush(s_exp[j - 1]);
-        sum.add(__uint_as_float(row.y), load_pack<B16, 8>(xc + (row.x & ~1u)));
+        if (first) b += __uint_as_float(row.y);
+        if (SUMS) sum.add(__uint_as_float(row.y), load_pack<B16, 8>(xc + (row.x & ~1u)));
     }
     flush(s_exp[n - 1]);
 }
 
-// Block (e, 512 columns): the sums of an expert whose rows lie in several chunks
-// (a quarter of the threads adds up a quarter of them, then the quarters in
-// order), and a zero row for an expert without any; the last block of an expert
-// sums dbias.
-__global__ void __launch_bounds__(kJoinThreads) route_join_kernel(const float* __restrict__ dlogits,
-                                                                  const int32_t* __restrict__ offsets,
-                                                                  const int32_t* __restrict__ row_pair, int P, int D,
+// Block (e, columns): the sums of an expert whose rows lie in several chunks (one
+// PARTS-th of them per share of the threads, then the shares in order), and a zero row
+// for an expert without any; the last block of an expert sums dbias.  Few experts have
+// many chunks each: 8,324 x 8 of 51 x 512 in 4 shares, with dbias from the pairs, 28 us
+// in all, in 16 shares 22 us.
+template <int PARTS>
+__global__ void __launch_bounds__(kJoinThreads) route_join_kernel(const int32_t* __restrict__ offsets, int P, int D,
                                                                   int chunk, const float* __restrict__ part,
+                                                                  const float* __restrict__ bias_part,
                                                                   float* __restrict__ dWr, float* __restrict__ dbias) {
-    __shared__ float sums[kJoinParts][kJoinCols];
+    constexpr int COLS = kJoinThreads / PARTS * 8;
+    __shared__ float sums[PARTS][COLS];
     pdl_wait();
     const int e = blockIdx.x;
     const int r0 = max(0, __ldg(offsets + e)), r1 = min(P, __ldg(offsets + e + 1));
+    // partial a is the expert's beginning (odd slot), the others' rows go on from the chunk before
+    const int a = r0 / chunk, b = (r1 - 1) / chunk;
+    if (r1 > r0 && a == b) return;              // stored by its block
     if (blockIdx.y == gridDim.y - 1) {
         if (!dbias) return;
         float s = 0.f;
-#pragma unroll 4
-        for (int j = r0 + threadIdx.x; j < r1; j += kJoinThreads) {
-            const int p = __ldg(row_pair + j);
-            s += p >= 0 && p < P ? __ldg(dlogits + p) : 0.f;
-        }
+        for (int i = a + threadIdx.x; r1 > r0 && i <= b; i += kJoinThreads) s += __ldg(bias_part + 2 * i + (i == a));
         s = warp_sum(s);
         if (threadIdx.x % 32 == 0) sums[0][threadIdx.x / 32] = s;
         __syncthreads();
@@ -364,14 +373,11 @@ __global__ void __launch_bounds__(kJoinThreads) route_join_kernel(const float* _
         }
         return;
     }
-    const int a = r0 / chunk, b = (r1 - 1) / chunk;
-    if (r1 > r0 && a == b) return;              // stored by its block
-    const int g = threadIdx.x / (kJoinCols / 8), col = threadIdx.x % (kJoinCols / 8) * 8;
-    const int c = blockIdx.y * kJoinCols;
+    const int g = threadIdx.x / (COLS / 8), col = threadIdx.x % (COLS / 8) * 8;
+    const int c = blockIdx.y * COLS;
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (r1 > r0 && c + col < D) {
-        // partial a is the expert's beginning (odd slot), the others' rows go on from the chunk before
-        const int each = (b - a + kJoinParts) / kJoinParts, i0 = a + g * each, i1 = min(b + 1, i0 + each);
+        const int each = (b - a + PARTS) / PARTS, i0 = a + g * each, i1 = min(b + 1, i0 + each);
 #pragma unroll 4
         for (int i = i0; i < i1; ++i) {
             float v[8];
@@ -382,10 +388,10 @@ __global__ void __launch_bounds__(kJoinThreads) route_join_kernel(const float* _
     }
     store_f32<float, 8>(&sums[g][col], acc);
     __syncthreads();
-    for (int i = threadIdx.x * 2; i < kJoinCols && c + i < D; i += kJoinThreads * 2) {
+    for (int i = threadIdx.x * 2; i < COLS && c + i < D; i += kJoinThreads * 2) {
         float s[2] = {0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < kJoinParts; ++j) {
+        for (int j = 0; j < PARTS; ++j) {
             s[0] += sums[j][i];
             s[1] += sums[j][i + 1];
         }
@@ -418,7 +424,7 @@ bool route_dense(int T, int E, int k) { return T >= kDenseMinT && (E <= 16 || (E
 size_t route_grad_ws_bytes(int T, int D, int E, int k) {
     if (route_dense(T, E, k)) return 256 + dense_part_bytes(T, D, E);
     const int P = T * k, chunk = P ? dw_chunk(P, D) : 16;
-    return 256 + (size_t)2 * ((P + chunk - 1) / chunk) * D * 4;
+    return 256 + (size_t)2 * ((P + chunk - 1) / chunk) * (D + 1) * 4;
 }
 
 size_t slice_smem(int E, int G) {
@@ -522,14 +528,19 @@ extern "C" moe_status moe_route_backward(const float* dgates, const float* gates
         return ops_status(launch_pdl(route_dw_small_kernel, dim3(E, dWr ? (D + kDwThreads * 8 - 1) / (kDwThreads * 8) : 1),
                                      dim3(D / 8 < kDwThreads ? D / 8 : kDwThreads), 0, s, (const float*)dlogits, xb, offsets,
                                      row_pair, T * k, D, k, dWr, dbias));
-    const int P = T * k, chunk = dw_chunk(P, D);
-    float* part = static_cast<float*>(ws);
-    if (dWr)
-        e = launch_pdl(route_dw_kernel, dim3((P + chunk - 1) / chunk, (D + kDwThreads * 8 - 1) / (kDwThreads * 8)),
-                       dim3(D / 8 < kDwThreads ? D / 8 : kDwThreads), (size_t)chunk * (sizeof(uint2) + sizeof(int)), s,
-                       (const float*)dlogits, ids, xb, offsets, row_pair, P, D, E, k, chunk, dWr, part);
+    const int P = T * k, chunk = dw_chunk(P, D), chunks = (P + chunk - 1) / chunk;
+    float *part = static_cast<float*>(ws), *bias_part = part + (size_t)2 * chunks * D;
+    auto sums = [&](auto kernel, int blocks, int threads) {
+        return launch_pdl(kernel, dim3(chunks, blocks), dim3(threads), (size_t)chunk * (sizeof(uint2) + sizeof(int)), s,
+                          (const float*)dlogits, ids, xb, offsets, row_pair, P, D, E, k, chunk, dWr, part, dbias, bias_part);
+    };
+    e = dWr ? sums(route_dw_kernel<true>, (D + kDwThreads * 8 - 1) / (kDwThreads * 8), D / 8 < kDwThreads ? D / 8 : kDwThreads)
+            : sums(route_dw_kernel<false>, 1, 32);
     if (e != cudaSuccess) return ops_status(e);
-    return ops_status(launch_pdl(route_join_kernel, dim3(E, (dWr ? (D + kJoinCols - 1) / kJoinCols : 0) + 1), dim3(kJoinThreads), 0, s,
-                                 (const float*)dlogits, offsets, row_pair, P, D, chunk, (const float*)part, dWr,
-                                 dbias));
+    auto join = [&](auto kernel, int parts) {
+        const int cols = kJoinThreads / parts * 8;
+        return ops_status(launch_pdl(kernel, dim3(E, (dWr ? (D + cols - 1) / cols : 0) + 1), dim3(kJoinThreads), 0, s, offsets,
+                                     P, D, chunk, (const float*)part, (const float*)bias_part, dWr, dbias));
+    };
+    return chunks >= kJoinFew * E ? join(route_join_kernel<16>, 16) : join(route_join_kernel<4>, 4);
 }
