@@ -246,11 +246,10 @@ struct Ring {
 // A thread's factors of its columns: w_post times a channel gate, and w_next
 // (1 where absent).  Kept in shared memory, a thread's N values in packs of four
 // that neighbouring threads hold next to one another (in registers the backward
-// pass spilled: 44 us against 40), or in registers where it is full.
-template <int N, bool KEPT>
+// pass spilled: 44 us against 40).
+template <int N>
 struct Factors {
     float4* at;                                 // [2][N / 4][threads per token]
-    float reg[KEPT ? 2 : 1][KEPT ? N : 1];
     int rank, size;
     template <typename Col, typename Args>
     MOE_DEVINL void make(const Col& col, const Args& a, bool write) {
@@ -265,34 +264,21 @@ struct Factors {
 #pragma unroll
         for (int j = 0; j < N; ++j) w[j] = 1.f;
         if (a.w_next) col.load(a.w_next, w);
-        if constexpr (KEPT) {
+        if (!write) return;
 #pragma unroll
-            for (int j = 0; j < N; ++j) reg[0][j] = v[j], reg[1][j] = w[j];
-        } else if (write) {
-#pragma unroll
-            for (int j = 0; j < N; j += 4) {
-                at[j / 4 * size + rank] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-                at[(N / 4 + j / 4) * size + rank] = make_float4(w[j], w[j + 1], w[j + 2], w[j + 3]);
-            }
+        for (int j = 0; j < N; j += 4) {
+            at[j / 4 * size + rank] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+            at[(N / 4 + j / 4) * size + rank] = make_float4(w[j], w[j + 1], w[j + 2], w[j + 3]);
         }
     }
     MOE_DEVINL void get(int n, float (&v)[N]) const {
-        if constexpr (KEPT) {
 #pragma unroll
-            for (int j = 0; j < N; ++j) v[j] = reg[n][j];
-        } else {
-#pragma unroll
-            for (int j = 0; j < N; j += 4) {
-                const float4 q = at[(n * (N / 4) + j / 4) * size + rank];
-                v[j] = q.x, v[j + 1] = q.y, v[j + 2] = q.z, v[j + 3] = q.w;
-            }
+        for (int j = 0; j < N; j += 4) {
+            const float4 q = at[(n * (N / 4) + j / 4) * size + rank];
+            v[j] = q.x, v[j + 1] = q.y, v[j + 2] = q.z, v[j + 3] = q.w;
         }
     }
 };
-
-// The widest fp32 rows leave no shared memory for the factors.
-template <typename T>
-constexpr bool kept_factors(bool smem_sums) { return smem_sums && sizeof(T) == 4; }
 
 template <typename T>
 MOE_DEVINL T* at_bytes(void* p, uint32_t at) { return reinterpret_cast<T*>(static_cast<char*>(p) + at); }
@@ -324,10 +310,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kNormThreads ? 3 : 1)
     pdl_wait();
 #pragma unroll
     for (int i = 0; i < STAGES; ++i) in.fetch(at + i * skip, t0 + i * step < a.T);
-    Factors<N, false> fac;
-    fac.at = reinterpret_cast<float4*>(dyn + groups * kSumFloats);
-    fac.rank = rank;
-    fac.size = a.group;
+    Factors<N> fac{reinterpret_cast<float4*>(dyn + groups * kSumFloats), rank, a.group};
     fac.make(col, a, g == 0);
     __syncthreads();
     const float inv = 1.f / a.D;
@@ -392,38 +375,25 @@ struct NormGradArgs {
 // of a token are formed at once, with one barrier.  A token gate stays outside
 // of q: sum(q G) is then its gradient.  A channel gate and w_post are the same
 // for all tokens, so both their gradients come from the sums of G yh.
-//   SMEM: the sums over tokens are kept in shared memory, for rows too wide for
-//   the registers.
-template <typename T, int N, int STAGES, int THREADS, bool SMEM, int KIND>
+template <typename T, int N, int STAGES, int THREADS, int KIND>
 __global__ void __launch_bounds__(THREADS)
     block_norm_backward_kernel(const __grid_constant__ NormGradArgs a) {
-    extern __shared__ __align__(16) float dyn[];        // the groups' sums, [2][D] over tokens, the factors, the rings
+    extern __shared__ __align__(16) float dyn[];        // the groups' sums, the factors, the groups' rings
     const int groups = blockDim.x / a.group, g = threadIdx.x / a.group, rank = threadIdx.x % a.group;
     const int step = gridDim.x * groups, t0 = blockIdx.x * groups + g;
     Group grp{g, rank, a.group, dyn + g * kSumFloats};
     const Cols<T, N, KIND> col{rank, a.group, a.D};
-    constexpr bool KEPT = kept_factors<T>(SMEM);
-    float* sums = dyn + groups * kSumFloats;
-    const int sums_floats = SMEM ? (2 * a.D + 3) / 4 * 4 : 0;
-    char* rings = reinterpret_cast<char*>(sums + sums_floats + (KEPT ? 0 : 2 * N * a.group));
+    char* rings = reinterpret_cast<char*>(dyn + groups * kSumFloats + 2 * N * a.group);
     Ring<T, N, 4, STAGES, KIND, NormGradArgs> in{a, col, rings + g * STAGES * 4 * a.pitch};
     const uint32_t skip = step * a.D * (uint32_t)sizeof(T);
     uint32_t at = t0 * a.D * (uint32_t)sizeof(T);
-    constexpr int M = SMEM ? 2 : N;
-    float s_next[M], s_gy[M];
+    float s_next[N], s_gy[N];                   // the sums over tokens
 #pragma unroll
-    for (int j = 0; j < M; ++j) s_next[j] = s_gy[j] = 0.f;
-    if (SMEM) {
-        for (int i = threadIdx.x; i < 2 * a.D; i += blockDim.x) sums[i] = 0.f;
-        __syncthreads();
-    }
+    for (int j = 0; j < N; ++j) s_next[j] = s_gy[j] = 0.f;
     pdl_wait();
 #pragma unroll
     for (int i = 0; i < STAGES; ++i) in.fetch(at + i * skip, t0 + i * step < a.T);
-    Factors<N, KEPT> fac;
-    fac.at = reinterpret_cast<float4*>(sums + sums_floats);
-    fac.rank = rank;
-    fac.size = a.group;
+    Factors<N> fac{reinterpret_cast<float4*>(dyn + groups * kSumFloats), rank, a.group};
     fac.make(col, a, g == 0);
     __syncthreads();
     const float inv = 1.f / a.D;
@@ -450,14 +420,7 @@ __global__ void __launch_bounds__(THREADS)
             in.read(0, at, xh);
             in.read(1, at, m);
             mul(xh, xh, rx);
-            if constexpr (!SMEM) {
-                fma(s_next, m, xh, s_next);
-            } else if (a.want_next) {
-                float acc[N];
-                col.load(sums, acc);
-                fma(acc, m, xh, acc);
-                col.store(sums, acc);
-            }
+            fma(s_next, m, xh, s_next);
             fac.get(1, w);
             mul(m, m, w);                       // u
             s0 = dot(xh, m);
@@ -483,13 +446,7 @@ __global__ void __launch_bounds__(THREADS)
             col.store(at_bytes<T>(a.dresidual, at), m);
         }
         if (per_token) mul(b, b, gt);
-        if constexpr (!SMEM) {
-            fma(s_gy, b, yh, s_gy);
-        } else if (a.want_post) {
-            col.load(sums + a.D, m);
-            fma(m, b, yh, m);
-            col.store(sums + a.D, m);
-        }
+        fma(s_gy, b, yh, s_gy);
         fac.get(0, w);
         mul(b, b, w);
         if (post) fma(b, yh, -c2, b);
@@ -499,10 +456,7 @@ __global__ void __launch_bounds__(THREADS)
     }
     // The block's sums: those of its groups added in order.
     float* part = a.part + (size_t)blockIdx.x * 2 * a.D;
-    if constexpr (SMEM) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < 2 * a.D; i += blockDim.x) part[i] = sums[i];
-    } else if (groups == 1) {
+    if (groups == 1) {
         if (a.want_next) col.store(part, s_next);
         if (a.want_post) col.store(part + a.D, s_gy);
     } else {
@@ -581,9 +535,9 @@ cudaError_t run_norm(NormArgs a, cudaStream_t s) {
     return launch_pdl(kernel, dim3(n.blocks(a.T, device_sm_count() * per_sm)), dim3(n.group * n.groups),
                       (size_t)n.groups * (kSumFloats * 4 + STAGES * 2 * n.pitch) + (size_t)n.group * N * 8, s, a);
 }
-template <typename T, int N, int STAGES, int THREADS, bool SMEM, int KIND>
+template <typename T, int N, int STAGES, int THREADS, int KIND>
 cudaError_t run_norm_backward(NormGradArgs a, int* blocks, cudaStream_t s) {
-    auto kernel = block_norm_backward_kernel<T, N, STAGES, THREADS, SMEM, KIND>;
+    auto kernel = block_norm_backward_kernel<T, N, STAGES, THREADS, KIND>;
     const NormShape n(a.D, N, sizeof(T), KIND >= WIDE, THREADS);
     static std::atomic<uint64_t> set{0};
     if (!once_per_device(set, [&] {
@@ -594,16 +548,15 @@ cudaError_t run_norm_backward(NormGradArgs a, int* blocks, cudaStream_t s) {
     a.group = n.group;
     a.pitch = n.pitch;
     *blocks = n.blocks(a.T, device_sm_count() < kNormParts ? device_sm_count() : kNormParts);
-    const size_t sums = SMEM ? (size_t)(2 * a.D + 3) / 4 * 16 : 0;
-    const size_t factors = kept_factors<T>(SMEM) ? 0 : (size_t)n.group * N * 8;
     return launch_pdl(kernel, dim3(*blocks), dim3(n.group * n.groups),
-                      sums + factors + (size_t)n.groups * (kSumFloats * 4 + STAGES * 4 * n.pitch), s, a);
+                      (size_t)n.groups * (kSumFloats * 4 + STAGES * 4 * n.pitch) + (size_t)n.group * N * 8, s, a);
 }
 
 // A thread has 16 bytes of a row (twice that for fp32 rows beyond 4,096).  Forward
 // blocks of 384 threads leave room for three per SM; 768 threads of the backward
-// pass, two tokens or more, for the sums over tokens in registers.  Beyond 4,096
-// elements those go to shared memory.
+// pass, two tokens or more, for the sums over tokens in registers.  Those of rows
+// beyond 4,096 elements need 16 elements per thread and 512 threads (3,072 x 8,192
+// bf16 62 us; 8 elements with the sums in shared memory 81 us).
 template <typename T, int KIND>
 cudaError_t pick_norm(const NormArgs& a, cudaStream_t s) {
     constexpr int N = 16 / sizeof(T);
@@ -617,19 +570,21 @@ cudaError_t pick_norm(const NormArgs& a, cudaStream_t s) {
 template <typename T, int KIND>
 cudaError_t pick_norm_backward(const NormGradArgs& a, int* blocks, cudaStream_t s) {
     constexpr int N = 16 / sizeof(T);
-    if (a.D <= kGradThreads / 2 * N) return run_norm_backward<T, N, 3, kGradThreads, false, KIND>(a, blocks, s);
-    if (a.D <= 512 * N) return run_norm_backward<T, N, 3, 512, false, KIND>(a, blocks, s);
-    if constexpr (N == 8) {
-        return run_norm_backward<T, N, 1, 1024, true, KIND>(a, blocks, s);
-    } else {
-        if (a.D <= 1024 * N) return run_norm_backward<T, N, 2, 1024, false, KIND>(a, blocks, s);
-        return run_norm_backward<T, 8, 1, 1024, true, KIND>(a, blocks, s);
+    if (a.D <= kGradThreads / 2 * N) return run_norm_backward<T, N, 3, kGradThreads, KIND>(a, blocks, s);
+    if (a.D <= 512 * N) return run_norm_backward<T, N, 3, 512, KIND>(a, blocks, s);
+    if constexpr (N == 4) {
+        if (a.D <= 1024 * N) return run_norm_backward<T, N, 2, 1024, KIND>(a, blocks, s);
     }
+    if constexpr (KIND == FULL) return cudaErrorInvalidValue;           // not beyond 4096: see whole_groups
+    else return run_norm_backward<T, 16, N / 4, 512, KIND>(a, blocks, s);
 }
 
 // Whether every thread of the groups has all its columns: D a multiple of 32 N,
-// with the N that the D takes above.
-bool whole_groups(int D, size_t elem) { return D % (elem == 4 && D <= 4096 ? 128 : 256) == 0; }
+// with the N that the D takes above.  Not for the widest rows' gradient: its
+// registers spill in that form (3,072 x 8,192 bf16 73 us against 62 us).
+bool whole_groups(int D, size_t elem, bool grad) {
+    return !(grad && D > 4096) && D % (elem == 4 && D <= 4096 ? 128 : 256) == 0;
+}
 
 moe_status norm_shapes(int T, int D) { return ops_shapes(T, 1, D); }
 
@@ -671,7 +626,7 @@ extern "C" moe_status moe_block_norm(const void* y, const void* residual, const 
     };
     const bool wide = units(16, 16), pairs = units(4, 8);
     const bool full =
-        wide && whole_groups(D, es) && residual && w_post && w_next && x_out && gate_mode != MOE_GATE_TOKEN;
+        wide && whole_groups(D, es, false) && residual && w_post && w_next && x_out && gate_mode != MOE_GATE_TOKEN;
     const NormArgs a{{y, residual}, gate, gate_mode, alpha, w_post, w_next,   eps,
                      T,             D,    0,         0,     x_out,  normed,   rstd_post, rstd_next};
     cudaStream_t s = (cudaStream_t)stream;
@@ -728,7 +683,7 @@ extern "C" moe_status moe_block_norm_backward(const void* dx_out, const void* dn
     };
     const bool wide = units(16, 16), pairs = units(4, 8);
     const bool per_token = gate_mode == MOE_GATE_TOKEN;
-    const bool full = wide && whole_groups(D, es) && dx_out && w_post && w_next && dresidual && !per_token;
+    const bool full = wide && whole_groups(D, es, true) && dx_out && w_post && w_next && dresidual && !per_token;
     const NormGradArgs a{{w_next ? x_out : nullptr, w_next ? dnormed : nullptr, dx_out, w_post || dgate ? y : nullptr},
                          gate, gate_mode, alpha, w_post, rstd_post, w_next, rstd_next, T, D, 0, 0, dy, dresidual,
                          per_token ? dgate : nullptr, dw_next != nullptr, dw_post || dgate_cols,
