@@ -35,6 +35,16 @@ CASES = [
     (301, 1026, BF, "channel", True, True, True, 1.0, 2),
     (150, 2048, BF, "none", True, True, True, 1.0, 2),
     (5, 6002, HF, "channel", True, False, True, 1.414, 0),
+    (701, 321, HF, "token", True, True, True, 0.25, 0),     # rows that start in turn on a pair and inside one
+    (301, 1023, BF, "channel", True, True, True, 1.0, 3),
+    (150, 3071, BF, "none", True, True, True, 1.0, 0),
+    (1, 3071, HF, "channel", True, True, True, 1.0, 1),
+    (2, 3072, BF, "channel", True, True, True, 1.0, 1),
+    (5, 6001, HF, "channel", True, False, True, 1.414, 0),
+    (3, 4095, BF, "token", False, True, True, 1.0, 0),
+    (4, 8192, BF, "channel", True, True, True, 1.0, 1),
+    (7301, 17, BF, "token", True, True, True, 1.0, 0),
+    (900, 1, HF, "channel", True, True, True, 1.0, 0),
     (7300, 18, BF, "token", True, True, True, 1.0, 0),      # 24 tokens in a block
     (7300, 24, BF, "channel", True, True, True, 1.0, 0),
 ]
@@ -83,7 +93,7 @@ def test_forward(case):
         moe.moe_block_norm(**a, normed=lone, eps=EPS)
         assert torch.equal(lone, o["normed"])
         if res:
-            b = dict(a, residual=a["residual"].clone())
+            b = dict(a, residual=shifted((T, D), dt, off, fill=0.0).copy_(a["residual"]))   # laid out alike
             moe.moe_block_norm(**b, x_out=b["residual"], normed=lone, eps=EPS)
             assert torch.equal(lone, o["normed"]) and torch.equal(b["residual"], o["x_out"])
         # two calls: the block's end, then the next block's norm
@@ -129,6 +139,24 @@ def test_backward(case):
                 moe.block_norm_backward_workspace_size(T, D)), dresidual=b, alpha=alpha, gate=a["gate"], gate_mode=mode,
                 w_post=a["w_post"], w_next=a["w_next"], rstd_post=o["rstd_post"], rstd_next=o["rstd_next"])
             assert torch.equal(b, g["dresidual"]) and torch.equal(few["dy"], g["dy"])
+
+
+@pytest.mark.parametrize("T,D,dt", [(300, 1000, BF), (5, 6001, HF), (700, 33, BF), (20, 3072, HF)])
+def test_matrices_that_start_differently(T, D, dt):
+    """Outputs and inputs at different offsets from a 4-byte boundary: single elements."""
+    case = (T, D, dt, "channel", True, True, True, 0.5, 1)
+    a = make(case, 5)
+    o = forward(a, 0)
+    x, err, _ = ref.norm(f64(a["y"]), f64(a["residual"]), 0.5, f64(a["gate"]), "channel", f64(a["w_post"]), EPS)
+    check(o["x_out"], x, stored(x, err, dt), "x_out")
+    n, e, _ = ref.next_norm(f64(o["x_out"]), f64(a["w_next"]), EPS)
+    check(o["normed"], n, stored(n, e, dt), "normed")
+    dx_out, dn = shifted((T, D), dt, 2, seed=20), shifted((T, D), dt, 3, seed=21)
+    g = backward(a, o, dx_out, dn, 0)
+    want = ref.norm_backward(f64(dx_out), f64(dn), f64(o["x_out"]), f64(a["y"]), 0.5, f64(a["gate"]), "channel",
+                             f64(a["w_post"]), f64(a["w_next"]), EPS)
+    for n, (v, e) in want.items():
+        check(g[n], v, stored(v, e, dt if n in ("dy", "dresidual") else FL), n)
 
 
 @pytest.mark.parametrize("mode", ["none", "channel", "token"])
