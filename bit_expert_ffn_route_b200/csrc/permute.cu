@@ -31,7 +31,8 @@ constexpr int kSmallPairs = 2816;          // up to here every block makes its p
                                            // 3,072 bf16: 8.6 us against 11.1 us with the plan; 4,000: 15.6 against 11.0)
 constexpr int kSmallThreads = 256;
 constexpr int kNoExpert = 0x7fffffff;
-constexpr int kShiftBytes = 256;           // rows that start anywhere: moved in shifted blocks from this length on
+constexpr int kShiftBytes = 256;           // rows that start anywhere: moved in shifted blocks from this length on,
+constexpr int kShiftCopyBytes = 512;       // and copied so from this on
 constexpr int kCopyThreads = 256;          // of a block that copies several short tokens
 constexpr int kSumThreads = 128;           // of an unpermute block
 constexpr int kDotThreads = 256;           // of a block of its gradient
@@ -262,7 +263,8 @@ __global__ void __launch_bounds__(kSmallThreads) permute_small_kernel(
 }
 
 // The copies behind the plan, and row_pair: a block per token, or `each` threads
-// where rows are SHORT (12,525 tokens x 12 x 32 fp16: 16 us against 22 us).  The
+// where rows are SHORT (12,525 tokens x 12 x 32 fp16: 16 us against 22 us; 10,019 x
+// 8 x 81 fp32 18 us, in shifted blocks 21 us; x 576 bf16 31 us against 28 us).  The
 // first columns of x are read while the plan is still made: its blocks let this
 // kernel start once they have waited for the kernels that may have written x.
 // 4,096 tokens x 10 x 3,072 bf16: 44 us, 277 MB at 6.3 TB/s.
@@ -758,12 +760,12 @@ moe_status launch_permute(const int32_t* ids, int T_, int k, int E, const int32_
                                      (size_t)kPlanWarps * ((E + 1) / 2 * 2) * 4, s, ids, P, E, slot_table, n_slots,
                                      offsets, pair_row, x ? nullptr : row_pair);
     if (e != cudaSuccess || !x) return ops_status(e);
-    if (!wide && D * (int)sizeof(T) >= kShiftBytes)
+    if (!wide && D * (int)sizeof(T) >= kShiftCopyBytes)
         return ops_status(launch_pdl(permute_rows_shifted_kernel<T>, dim3(T_), dim3(row_threads(D / V)),
                                      staged_bytes(D, sizeof(T)), s, x, (const int32_t*)pair_row, T_, k, D, rows,
                                      row_pair));
     const int packs = wide ? D / V : D;
-    const bool few = packs <= 64;
+    const bool few = packs <= (wide ? 64 : 128);
     const int each = few ? threads_for(packs, 8, 64) : row_threads(packs), tokens = few ? kCopyThreads / each : 1;
     auto kernel = wide ? (few ? permute_rows_kernel<T, V, true> : permute_rows_kernel<T, V, false>)
                        : (few ? permute_rows_kernel<T, 1, true> : permute_rows_kernel<T, 1, false>);
