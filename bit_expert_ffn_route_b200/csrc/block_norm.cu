@@ -376,7 +376,7 @@ struct NormGradArgs {
 // of q: sum(q G) is then its gradient.  A channel gate and w_post are the same
 // for all tokens, so both their gradients come from the sums of G yh.
 template <typename T, int N, int STAGES, int THREADS, int KIND>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(THREADS, 1)
     block_norm_backward_kernel(const __grid_constant__ NormGradArgs a) {
     extern __shared__ __align__(16) float dyn[];        // the groups' sums, the factors, the groups' rings
     const int groups = blockDim.x / a.group, g = threadIdx.x / a.group, rank = threadIdx.x % a.group;
