@@ -137,9 +137,9 @@ def test_behind_the_router_against_differences(T):
         assert abs(num - (g * v).sum()) <= tol, (n, num, (g * v).sum(), tol)
 
 
-@pytest.mark.parametrize("T", [20, 64, 900])
-def test_captured(T):
-    k, E, D = 4, 16, 512
+@pytest.mark.parametrize("T,E", [(20, 16), (64, 16), (900, 16), (20, 100), (900, 100), (4000, 100)])
+def test_captured(T, E):
+    k, D = 4, 512
     a, b = make(T, k, E, D, "distinct", 1), make(T, k, E, D, "distinct", 2)
     hold = [t.clone() for t in a[:5]]
     o, pr, rp, _ = buffers(T, k, E)
