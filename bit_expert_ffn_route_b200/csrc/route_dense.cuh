@@ -369,14 +369,19 @@ __global__ void __launch_bounds__(256) route_dense_join_kernel(const float* __re
 }
 
 // Tokens of a block: about a wave of blocks.
+inline int dense_chunks(int D, int E) {
+    const int chunks = (E <= 16 ? kDenseBlocks16 : kDenseBlocks) / (D / kDenseCols);
+    return chunks < 1 ? 1 : chunks;
+}
 inline int dense_chunk(int T, int D, int E) {
-    int chunks = (E <= 16 ? kDenseBlocks16 : kDenseBlocks) / (D / kDenseCols);
-    if (chunks < 1) chunks = 1;
+    const int chunks = dense_chunks(D, E);
     return ((T + chunks - 1) / chunks + kDenseTok - 1) / kDenseTok * kDenseTok;
 }
+// Of the partials of T tokens and of fewer: whole tiles per block leave at most this many blocks, and sometimes fewer
+// of more tokens.
 inline size_t dense_part_bytes(int T, int D, int E) {
-    const int chunk = dense_chunk(T, D, E);
-    return (size_t)((T + chunk - 1) / chunk) * ((size_t)E * D + (E + 3) / 4 * 4) * 4;
+    const int tiles = (T + kDenseTok - 1) / kDenseTok, chunks = dense_chunks(D, E);
+    return (size_t)(tiles < chunks ? tiles : chunks) * ((size_t)E * D + (E + 3) / 4 * 4) * 4;
 }
 
 template <int EP>

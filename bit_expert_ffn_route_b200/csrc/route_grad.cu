@@ -421,10 +421,18 @@ moe_status route_grad_shapes(int T, int D, int E, int k) {
 // and 13.0; of 64 (an experts' tile twice as wide) 4,096 x 8 x 2,048 38 and 34.
 bool route_dense(int T, int E, int k) { return T >= kDenseMinT && (E <= 16 || (E <= kDenseMaxE && k >= 5)); }
 
+// What T tokens need and fewer: the chunks are no more than the blocks of 16 rows, and than kDwSums / D or what chunks
+// of the greatest length leave.  Their own number falls wherever a chunk becomes longer.
+size_t dw_part_bytes(int P, int D) {
+    int chunks = kDwSums / D;
+    if (chunks < (P + kDwMaxChunk - 1) / kDwMaxChunk) chunks = (P + kDwMaxChunk - 1) / kDwMaxChunk;
+    if (chunks > (P + 15) / 16) chunks = (P + 15) / 16;
+    return (size_t)2 * chunks * (D + 1) * 4;
+}
 size_t route_grad_ws_bytes(int T, int D, int E, int k) {
-    if (route_dense(T, E, k)) return 256 + dense_part_bytes(T, D, E);
-    const int P = T * k, chunk = P ? dw_chunk(P, D) : 16;
-    return 256 + (size_t)2 * ((P + chunk - 1) / chunk) * (D + 1) * 4;
+    if (!route_dense(T, E, k)) return 256 + dw_part_bytes(T * k, D);
+    const size_t dense = dense_part_bytes(T, D, E), few = dw_part_bytes((kDenseMinT - 1) * k, D);
+    return 256 + (dense > few ? dense : few);
 }
 
 size_t slice_smem(int E, int G) {

@@ -32,7 +32,9 @@
  *    once, when they are stored.
  *  - Outputs alias neither inputs nor one another unless stated.
  *  - Workspaces need no initialisation and hold nothing between calls; calls
- *    sharing one must not overlap on the device.
+ *    sharing one must not overlap on the device.  Their sizes never fall as T
+ *    grows: one for the most tokens serves every smaller batch of the same D, E
+ *    and k.
  *  - Limits (MOE_ERR_UNSUPPORTED beyond): 1 <= D <= 8192, 1 <= k <= 16,
  *    1 <= E <= 1024, 0 <= T <= 65536.  T == 0 is valid.
  */
