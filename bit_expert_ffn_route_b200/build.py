@@ -75,7 +75,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         for out in ex.map(run, jobs):
             if verbose and out:
                 sys.stderr.write(out)
-    if force or _stale(LIB, objs):
+    if force or jobs or _stale(LIB, objs):
         subprocess.run([NVCC, *ARCH, "-shared", "-o", LIB, *objs, "-lcudart"], check=True)
     if force or _stale(OPS, [OPS_SRC, LIB] + headers):
         run(_ops_command())

@@ -1,0 +1,66 @@
+"""What build.build() compiles and links, with the compilers replaced by a record
+of their commands (nothing is compiled here)."""
+import os
+import subprocess
+
+import pytest
+
+from bit_expert_ffn_route_b200 import build
+
+TICK = 1_700_000_000
+
+
+class Tree:
+    """A source tree of one kernel file and the binding; compilers that write their output at the time `now`."""
+
+    def __init__(self, root, monkeypatch):
+        for name in ("csrc", "include", "_build"):
+            (root / name).mkdir()
+        self.now, self.ran, self.fails = TICK, [], ()
+        self.files = {"cu": root / "csrc" / "a.cu", "h": root / "include" / "a.h", "cpp": root / "csrc" / "binding.cpp"}
+        for f in self.files.values():
+            self.touch(f)
+        for name, at in dict(CSRC="csrc", INCLUDE="include", BUILD="_build", LIB="libmoe.so", OPS="_ops.so",
+                             OPS_SRC="csrc/binding.cpp").items():
+            monkeypatch.setattr(build, name, str(root / at))
+        monkeypatch.setattr(build.subprocess, "run", self.run)
+
+    def touch(self, f):
+        with open(f, "w") as out:
+            out.write("x")
+        os.utime(f, (self.now, self.now))
+
+    def run(self, cmd, **_):
+        out = os.path.basename(cmd[cmd.index("-o") + 1])
+        self.ran.append(out)
+        if out in self.fails:
+            return subprocess.CompletedProcess(cmd, 1, "", "no such header")
+        self.touch(cmd[cmd.index("-o") + 1])
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    def build(self, **kw):
+        self.ran = []
+        build.build(**kw)
+        return self.ran
+
+
+@pytest.fixture
+def tree(tmp_path, monkeypatch):
+    return Tree(tmp_path, monkeypatch)
+
+
+def test_what_is_newer_is_built_again(tree):
+    assert tree.build() == ["a.o", "libmoe.so", "_ops.so"]
+    assert tree.build() == []
+    tree.now += 1
+    tree.touch(tree.files["cpp"])
+    assert tree.build() == ["_ops.so"]
+    assert tree.build(force=True) == ["a.o", "libmoe.so", "_ops.so"]
+
+
+def test_every_object_that_is_built_is_linked(tree):
+    """Also where the file system's clock shows it no younger than the library: built in the library's own tick."""
+    tree.now += 5
+    tree.build()
+    os.remove(os.path.join(build.BUILD, "a.o"))
+    assert tree.build()[:2] == ["a.o", "libmoe.so"]
