@@ -3,7 +3,9 @@ native binding of moe_ops.h (_ops.so, a Python extension module), in-tree.
 
     python -m bit_expert_ffn_route_b200.build [--force]
 
-nvcc cross-compiles here without a GPU; the .so lands next to this file.
+nvcc cross-compiles here without a GPU; the .so lands next to this file.  The
+extension module needs a C++ compiler and torch's headers: without them the build
+warns, and moe.py raises at the first use of one of its calls.
 """
 from __future__ import annotations
 
@@ -11,6 +13,7 @@ import glob
 import os
 import subprocess
 import sys
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -78,7 +81,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if force or jobs or _stale(LIB, objs):
         subprocess.run([NVCC, *ARCH, "-shared", "-o", LIB, *objs, "-lcudart"], check=True)
     if force or _stale(OPS, [OPS_SRC, LIB] + headers):
-        run(_ops_command())
+        try:
+            run(_ops_command())
+        except (RuntimeError, OSError, ImportError) as e:       # the compiler's errors, no compiler, no torch
+            if os.path.exists(OPS):             # made from other sources: not to be loaded
+                os.remove(OPS)
+            warnings.warn(f"{OPS} was not built: the calls of moe_ops.h cannot be used from Python ({e})",
+                          RuntimeWarning)
     return LIB
 
 

@@ -2,10 +2,12 @@
 of their commands (nothing is compiled here)."""
 import os
 import subprocess
+import sys
 
 import pytest
 
-from bit_expert_ffn_route_b200 import build
+import bit_expert_ffn_route_b200
+from bit_expert_ffn_route_b200 import build, moe
 
 TICK = 1_700_000_000
 
@@ -64,3 +66,31 @@ def test_every_object_that_is_built_is_linked(tree):
     tree.build()
     os.remove(os.path.join(build.BUILD, "a.o"))
     assert tree.build()[:2] == ["a.o", "libmoe.so"]
+
+
+@pytest.mark.parametrize("how", ["compile error", "no compiler"])
+def test_without_the_extension_module(tree, how, monkeypatch):
+    """libmoe.so is built all the same, with a warning; the calls of moe_ops.h raise at their first use, and an
+    extension module of older sources does not stay."""
+    tree.build()
+    tree.now += 1
+    for f in tree.files.values():
+        tree.touch(f)
+    if how == "compile error":
+        tree.fails = ("_ops.so",)
+    else:
+        monkeypatch.setattr(build, "_ops_command", lambda: (_ for _ in ()).throw(FileNotFoundError("g++")))
+    with pytest.warns(RuntimeWarning, match="_ops.so was not built"):
+        assert build.build() == build.LIB
+    assert not os.path.exists(build.OPS) and os.path.getmtime(build.LIB) == tree.now
+    with pytest.warns(RuntimeWarning):          # tried again by the next build
+        build.build()
+
+
+def test_a_call_without_the_extension_module(monkeypatch):
+    """The import fails (None in sys.modules) as it does where the file is missing."""
+    monkeypatch.setattr(moe, "lib", lambda: None)
+    monkeypatch.setitem(sys.modules, "bit_expert_ffn_route_b200._ops", None)
+    monkeypatch.delattr(bit_expert_ffn_route_b200, "_ops", raising=False)
+    with pytest.raises(RuntimeError, match="_ops.so is missing"):
+        moe.__getattr__("moe_permute")
