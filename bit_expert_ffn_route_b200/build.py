@@ -23,6 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
 OPS_SRC, OPS = os.path.join(CSRC, "binding.cpp"), os.path.join(HERE, "_ops.so")
+OPS_FOR = os.path.join(BUILD, "_ops.for")       # the versions of torch and Python that it was built for
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -44,6 +45,13 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _read(path):
+    if not os.path.exists(path):
+        return None
+    with open(path) as f:
+        return f.read()
+
+
 def _ops_command():
     import sysconfig
 
@@ -52,7 +60,8 @@ def _ops_command():
     include = [os.path.join(at, "include"), os.path.join(at, "include", "torch", "csrc", "api", "include"),
                sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
-            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE,
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+            f'-DMOE_TORCH_VERSION="{torch.__version__}"', "-I", INCLUDE,
             *(f"-isystem{i}" for i in include), OPS_SRC, "-o", OPS, "-L" + os.path.join(at, "lib"), "-ltorch_python",
             "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L" + HERE, "-l:libmoe.so", "-Wl,-rpath,$ORIGIN"]
 
@@ -80,14 +89,17 @@ def build(force: bool = False, verbose: bool = False) -> str:
                 sys.stderr.write(out)
     if force or jobs or _stale(LIB, objs):
         subprocess.run([NVCC, *ARCH, "-shared", "-o", LIB, *objs, "-lcudart"], check=True)
-    if force or _stale(OPS, [OPS_SRC, LIB] + headers):
-        try:
-            run(_ops_command())
-        except (RuntimeError, OSError, ImportError) as e:       # the compiler's errors, no compiler, no torch
-            if os.path.exists(OPS):             # made from other sources: not to be loaded
+    try:
+        import torch
+        versions = f"torch {torch.__version__}, Python {sys.version_info[0]}.{sys.version_info[1]}"
+        if force or _stale(OPS, [OPS_SRC, LIB] + headers) or _read(OPS_FOR) != versions:
+            if os.path.exists(OPS):             # of other sources, or for another torch: not to be loaded
                 os.remove(OPS)
-            warnings.warn(f"{OPS} was not built: the calls of moe_ops.h cannot be used from Python ({e})",
-                          RuntimeWarning)
+            run(_ops_command())
+            with open(OPS_FOR, "w") as f:
+                f.write(versions)
+    except (RuntimeError, OSError, ImportError) as e:           # the compiler's errors, no compiler, no torch
+        warnings.warn(f"{OPS} was not built: the calls of moe_ops.h cannot be used from Python ({e})", RuntimeWarning)
     return LIB
 
 

@@ -348,7 +348,27 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ops", "The calls of moe_ops.h on 
 
 }  // namespace
 
+// The module reads tensors through functions that the compiler put into it, and its own objects lie as this
+// Python's headers say: with another torch or Python it refuses to load.  Only calls of Python's stable ABI here.
+static bool built_for_this_process() {
+    const std::string python = std::to_string(PY_MAJOR_VERSION) + "." + std::to_string(PY_MINOR_VERSION) + ".";
+    if (std::string(Py_GetVersion()).compare(0, python.size(), python) != 0) {
+        PyErr_Format(PyExc_ImportError, "_ops.so was built for Python %s, not %s", PY_VERSION, Py_GetVersion());
+        return false;
+    }
+    PyObject* torch = PyImport_ImportModule("torch");
+    PyObject* version = torch ? PyObject_GetAttrString(torch, "__version__") : nullptr;
+    PyObject* text = version ? PyObject_Str(version) : nullptr;
+    const int differs = text ? PyUnicode_CompareWithASCIIString(text, MOE_TORCH_VERSION) : 1;
+    if (text && differs) PyErr_Format(PyExc_ImportError, "_ops.so was built for torch %s, not %U", MOE_TORCH_VERSION, text);
+    Py_XDECREF(text);
+    Py_XDECREF(version);
+    Py_XDECREF(torch);
+    return !differs;
+}
+
 PyMODINIT_FUNC PyInit__ops() {
+    if (!built_for_this_process()) return nullptr;
     for (Signature* s : {&kPermute, &kPermuteBackward, &kUnpermute, &kUnpermuteBackward, &kRouteBackward, &kBlockNorm, &kBlockNormBackward})
         for (int i = 0; i < s->n; ++i)
             if (!(s->interned[i] = PyUnicode_InternFromString(s->params[i]))) return nullptr;

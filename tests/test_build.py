@@ -5,6 +5,7 @@ import subprocess
 import sys
 
 import pytest
+import torch
 
 import bit_expert_ffn_route_b200
 from bit_expert_ffn_route_b200 import build, moe
@@ -23,7 +24,7 @@ class Tree:
         for f in self.files.values():
             self.touch(f)
         for name, at in dict(CSRC="csrc", INCLUDE="include", BUILD="_build", LIB="libmoe.so", OPS="_ops.so",
-                             OPS_SRC="csrc/binding.cpp").items():
+                             OPS_SRC="csrc/binding.cpp", OPS_FOR="_build/_ops.for").items():
             monkeypatch.setattr(build, name, str(root / at))
         monkeypatch.setattr(build.subprocess, "run", self.run)
 
@@ -94,3 +95,22 @@ def test_a_call_without_the_extension_module(monkeypatch):
     monkeypatch.delattr(bit_expert_ffn_route_b200, "_ops", raising=False)
     with pytest.raises(RuntimeError, match="_ops.so is missing"):
         moe.__getattr__("moe_permute")
+
+
+def test_the_extension_module_is_built_for_one_torch(tree, monkeypatch):
+    """Another torch: built again, although no source is newer."""
+    assert "_ops.so" in tree.build()
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    assert tree.build() == ["_ops.so"]
+    assert tree.build() == []
+
+
+def test_the_extension_module_loads_with_its_torch_alone():
+    """With another version in its place the import fails, and a call says what to do; with its own it works."""
+    build.build()
+    code = ("import torch\n{}\nfrom bit_expert_ffn_route_b200 import moe\ntry: moe.moe_permute\n"
+            "except RuntimeError as e: print('refused', e, e.__cause__)\nelse: print('loaded')")
+    for change, want in (("", "loaded"), ("torch.__version__ = '2.99.0'", "refused")):
+        r = subprocess.run([sys.executable, "-c", code.format(change)], capture_output=True, text=True, cwd=build.ROOT)
+        assert r.returncode == 0 and r.stdout.startswith(want), (r.stdout, r.stderr)
+    assert "build --force" in r.stdout and "not 2.99.0" in r.stdout
