@@ -25,7 +25,8 @@ namespace cg = cooperative_groups;
 
 constexpr int kPlanThreads = 512;          // two experts per thread
 constexpr int kPlanWarps = kPlanThreads / 32;
-constexpr int kPlanBlocks = 16;            // one cluster (of the size that a kernel has to ask for)
+constexpr int kPlanBlocks = 16;            // one cluster (of the size that a kernel has to ask for), where one of
+constexpr int kPlanFewBlocks = 8;          // these fits on the device: a partition of one may have room for eight only
 constexpr int kPlanHeld = 8;               // rounds of 32 pairs that a warp loads together
 constexpr int kSmallPairs = 2816;          // up to here every block makes its part of the plan itself (2,500 pairs of
                                            // 3,072 bf16: 8.6 us against 11.1 us with the plan; 4,000: 15.6 against 11.0)
@@ -77,8 +78,9 @@ MOE_DEVINL int block_scan(int v, int* wsum) {
 // of the first 8 rounds stay in registers (those of longer segments wait in
 // pair_row): one walk does all the matching.  row_pair null: the next kernel
 // writes it (scattered words, which few SMs write slowly).  40,960 pairs take 8 us
-// alone, 6 us in front of the copies; a cluster of 8 blocks took 11 us.
-__global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThreads)
+// alone, 6 us in front of the copies; in a cluster of BLOCKS = 8 11 us.
+template <int BLOCKS>
+__global__ void __cluster_dims__(BLOCKS, 1, 1) __launch_bounds__(kPlanThreads)
     permute_plan_kernel(const int32_t* __restrict__ ids, int P, int E, const int32_t* __restrict__ slot_table,
                         int n_slots, int32_t* __restrict__ offsets, int32_t* __restrict__ pair_row,
                         int32_t* __restrict__ row_pair) {
@@ -92,7 +94,7 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
     for (int i = threadIdx.x; i < kPlanWarps * Ep / 2; i += kPlanThreads) reinterpret_cast<int2*>(count)[i] = {0, 0};
     pdl_wait();
     pdl_launch_dependents();
-    const int rounds = (P + kPlanBlocks * kPlanThreads - 1) / (kPlanBlocks * kPlanThreads);
+    const int rounds = (P + BLOCKS * kPlanThreads - 1) / (BLOCKS * kPlanThreads);
     const int p0 = (b * kPlanWarps + w) * rounds * 32 + lane;
     int32_t* mine = count + w * Ep;
     int key[kPlanHeld], rank[kPlanHeld];
@@ -157,12 +159,12 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
     cluster.sync();
     int2 total = {0, 0}, before = {0, 0};
     if (e0 < E) {
-        int2 c[kPlanBlocks];
+        int2 c[BLOCKS];
 #pragma unroll
-        for (int i = 0; i < kPlanBlocks; ++i)
+        for (int i = 0; i < BLOCKS; ++i)
             c[i] = *reinterpret_cast<const int2*>(cluster.map_shared_rank(block_total, i) + e0);
 #pragma unroll
-        for (int i = 0; i < kPlanBlocks; ++i) {
+        for (int i = 0; i < BLOCKS; ++i) {
             total.x += c[i].x, total.y += c[i].y;
             if (i < b) before.x += c[i].x, before.y += c[i].y;
         }
@@ -736,6 +738,55 @@ moe_status launch_unpermute(const void* rows, int n_rows, const int32_t* pair_ro
     });
 }
 
+constexpr size_t plan_smem(int E) { return (size_t)kPlanWarps * ((E + 1) / 2 * 2) * 4; }
+
+// The plan kernel's launch attributes on the current device
+template <int BLOCKS>
+bool plan_ready() {
+    static std::atomic<uint64_t> set{0};
+    return once_per_device(set, [] {
+        return cudaFuncSetAttribute(permute_plan_kernel<BLOCKS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)plan_smem(kOpsMaxE)) == cudaSuccess &&
+               (BLOCKS <= 8 || cudaFuncSetAttribute(permute_plan_kernel<BLOCKS>,
+                                                    cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess);
+    });
+}
+
+// The blocks of the plan on the current device: kPlanBlocks where such a cluster fits at all, looked up once per device.
+int plan_blocks() {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return kPlanFewBlocks;
+    const bool kept = dev >= 0 && dev < 64;
+    if (const int n = kept ? known[dev].load(std::memory_order_relaxed) : 0) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kPlanBlocks);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = plan_smem(kOpsMaxE);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim = {kPlanBlocks, 1, 1};
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if (!plan_ready<kPlanBlocks>() ||
+        cudaOccupancyMaxActiveClusters(&clusters, permute_plan_kernel<kPlanBlocks>, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        clusters = 0;
+    }
+    const int n = clusters > 0 ? kPlanBlocks : kPlanFewBlocks;
+    if (kept) known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+cudaError_t launch_plan(const int32_t* ids, int P, int E, const int32_t* slot_table, int n_slots, int32_t* offsets,
+                        int32_t* pair_row, int32_t* row_pair, int blocks, cudaStream_t s) {
+    if (!(blocks == kPlanBlocks ? plan_ready<kPlanBlocks>() : plan_ready<kPlanFewBlocks>())) return cudaErrorUnknown;
+    return launch_pdl(blocks == kPlanBlocks ? permute_plan_kernel<kPlanBlocks> : permute_plan_kernel<kPlanFewBlocks>,
+                      dim3(blocks), dim3(kPlanThreads), plan_smem(E), s, ids, P, E, slot_table, n_slots, offsets, pair_row,
+                      row_pair);
+}
+
 template <typename T>
 moe_status launch_permute(const int32_t* ids, int T_, int k, int E, const int32_t* slot_table, int n_slots,
                           const T* x, int D, T* rows, int32_t* offsets, int32_t* pair_row, int32_t* row_pair,
@@ -748,17 +799,8 @@ moe_status launch_permute(const int32_t* ids, int T_, int k, int E, const int32_
         return ops_status(launch_pdl(kernel, dim3(T_ + 1), dim3(kSmallThreads), 0, s, ids, P, E, slot_table, n_slots, x,
                                      k, D, rows, offsets, pair_row, row_pair));
     }
-    static std::atomic<uint64_t> set{0};
-    if (!once_per_device(set, [] {
-            return cudaFuncSetAttribute(permute_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        kPlanWarps * kOpsMaxE * 4) == cudaSuccess &&
-                   cudaFuncSetAttribute(permute_plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
-                       cudaSuccess;
-        }))
-        return MOE_ERR_CUDA;
-    const cudaError_t e = launch_pdl(permute_plan_kernel, dim3(kPlanBlocks), dim3(kPlanThreads),
-                                     (size_t)kPlanWarps * ((E + 1) / 2 * 2) * 4, s, ids, P, E, slot_table, n_slots,
-                                     offsets, pair_row, x ? nullptr : row_pair);
+    const cudaError_t e = launch_plan(ids, P, E, slot_table, n_slots, offsets, pair_row, x ? nullptr : row_pair,
+                                      plan_blocks(), s);
     if (e != cudaSuccess || !x) return ops_status(e);
     if (!wide && D * (int)sizeof(T) >= kShiftCopyBytes)
         return ops_status(launch_pdl(permute_rows_shifted_kernel<T>, dim3(T_), dim3(row_threads(D / V)),
@@ -800,6 +842,18 @@ extern "C" moe_status moe_permute(const int32_t* ids, int T, int k, int E, const
         return launch_permute<Tp>(ids, T, k, E, slot_table, n_slots, static_cast<const Tp*>(x), D,
                                   static_cast<Tp*>(rows), offsets, pair_row, row_pair, s);
     });
+}
+
+extern "C" moe_status moe_debug_permute_plan(const int32_t* ids, int T, int k, int E, int blocks, int32_t* offsets,
+                                             int32_t* pair_row, int32_t* row_pair, moe_stream_t stream) {
+    moe_status st = ops_shapes(T, k, 1);
+    if (st != MOE_OK) return st;
+    if (T == 0 || E <= 0 || (blocks != kPlanBlocks && blocks != kPlanFewBlocks)) return MOE_ERR_INVALID_ARG;
+    if (E > kOpsMaxE) return MOE_ERR_UNSUPPORTED;
+    if (!ids || !offsets || !pair_row || !row_pair) return MOE_ERR_INVALID_ARG;
+    if (!ops_aligned(ids, 4) || !ops_aligned(offsets, 4) || !ops_aligned(pair_row, 4) || !ops_aligned(row_pair, 4))
+        return MOE_ERR_INVALID_ARG;
+    return ops_status(launch_plan(ids, T * k, E, nullptr, 0, offsets, pair_row, row_pair, blocks, (cudaStream_t)stream));
 }
 
 extern "C" moe_status moe_unpermute(const void* rows, int n_rows, const int32_t* pair_row, const float* weights, int T,

@@ -32,7 +32,8 @@ EXPORTS = ["moe_slot_code_bytes", "moe_slot_scale_bytes", "moe_route_workspace_s
            "moe_debug_prefill_operand", "moe_layer_workspace_size", "moe_layer_forward",
            "moe_workspace_size_fp8", "moe_expert_forward_fp8", "moe_permute", "moe_permute_backward",
            "moe_unpermute", "moe_unpermute_backward", "moe_route_backward", "moe_route_backward_workspace_size",
-           "moe_block_norm", "moe_block_norm_backward", "moe_block_norm_backward_workspace_size"]
+           "moe_block_norm", "moe_block_norm_backward", "moe_block_norm_backward_workspace_size",
+           "moe_debug_permute_plan"]
 
 
 class MoeError(RuntimeError):
@@ -104,6 +105,8 @@ def lib():
         f = ctypes.c_float
         L.moe_permute.restype = i
         L.moe_permute.argtypes = [P, i, i, i, P, i, P, i, i, P, P, P, P, P]
+        L.moe_debug_permute_plan.restype = i
+        L.moe_debug_permute_plan.argtypes = [P, i, i, i, i, P, P, P, P]
         L.moe_permute_backward.restype = i
         L.moe_permute_backward.argtypes = [P, i, P, i, i, i, i, P, P]
         L.moe_unpermute.restype = i
@@ -241,6 +244,13 @@ def moe_debug_wait_flag(flag, expect, limit_us, ws, stream=None):
     """Test hook: a bounded device wait for flag[0] == expect (flag: int32/uint32 device tensor)."""
     _check("moe_debug_wait_flag", lib().moe_debug_wait_flag(_p(flag), int(expect), int(limit_us), _p(ws),
                                                             _stream(stream)))
+
+
+def moe_debug_permute_plan(ids, E, blocks, offsets, pair_row, row_pair, stream=None):
+    """Test hook: moe_permute's plan of all pairs by the kernel of large batches, in a cluster of 16 or 8 blocks."""
+    _check("moe_debug_permute_plan", lib().moe_debug_permute_plan(_p(ids), ids.shape[0], ids.shape[1], int(E),
+                                                                  int(blocks), _p(offsets), _p(pair_row), _p(row_pair),
+                                                                  _stream(stream)))
 
 
 def moe_debug_prefill_operand(pool: moe_pool, gemm, slot, m0, dump, stream=None):

@@ -72,6 +72,14 @@ moe_status moe_permute(const int32_t* ids, int T, int k, int E, const int32_t* s
                        moe_stream_t stream);
 
 /*
+ * Test hook: moe_permute's plan (no slot_table, no rows) by the kernel of large
+ * batches, in one cluster of `blocks` = 16, or of 8, which moe_permute takes where
+ * the device (a partition of one) has no room for 16.  T >= 1.
+ */
+moe_status moe_debug_permute_plan(const int32_t* ids, int T, int k, int E, int blocks, int32_t* offsets,
+                                  int32_t* pair_row, int32_t* row_pair, moe_stream_t stream);
+
+/*
  * Gradient of moe_permute's rows with respect to x:
  *   dx[t] = sum over r of drows[pair_row[t][r]], r ascending; 0 for a token
  *   without rows.
