@@ -1,6 +1,6 @@
 // rows.cuh — typed rows for the operators of moe_ops.h: element types, packs of
-// elements moved by one load or store, block sums, and the host-side choice of
-// pack width.
+// elements moved by one load or store, warp sums, and the host's checks of types,
+// alignment and limits.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -122,18 +122,6 @@ MOE_DEVINL void load_f32(const T* p, float (&f)[V]) {
         for (int j = 0; j < W; ++j) f[i + j] = g[j];
     }
 }
-// v as it reads back after a store as T
-template <typename T>
-MOE_DEVINL float as_stored(float v) {
-    if constexpr (sizeof(T) == 4) return v;
-    else {
-        const float f[2] = {v, 0.f};
-        float g[2];
-        unpack_word(T{}, pack_word(T{}, f), g);
-        return g[0];
-    }
-}
-
 MOE_DEVINL float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
