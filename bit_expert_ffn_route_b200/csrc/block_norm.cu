@@ -7,7 +7,7 @@
 // likewise: four rows in, two out.  HBM is the floor of both; what bounds them is
 // the chain of a token's steps (rows out of shared memory, a sum over the block's
 // warps, the rest) with as many warps as the registers leave.  4,096 tokens of
-// 3,072 bf16: 20 us forward (100 MB, 5.1 TB/s) and 36 us backward (151 MB, 4.2
+// 3,072 bf16: 19 us forward (100 MB, 5.3 TB/s) and 36 us backward (151 MB, 4.2
 // TB/s; 31 us of it the tokens, the rest the join of the partial sums).
 //
 // Threads: a group of whole warps takes a token, each thread the same columns of
@@ -145,11 +145,13 @@ struct Group {
 constexpr int kSumFloats = 256;
 
 // How rows lie: they start anywhere (ANY), they are of whole PAIRS of 16-bit
-// elements (13,519 x 2,482 fp16 forward 73 us, 92 us as single elements; 6,000 x
+// elements (13,519 x 2,482 fp16 forward 72 us, 92 us as single elements; 6,000 x
 // 6,002 bf16 backward 147 against 221) or of whole 16-byte packs (WIDE), or besides
 // every thread of the group has all its columns and the call has every operand but
 // a token gate (FULL: no test of these in the token's path; 4,096 x 3,072 bf16
-// forward 19.2 us against 21.3 us, backward 38 against 40).
+// forward 19.1 us against 21.7 us, backward 36 against 47; 12,288 x 2,048 backward 58
+// against 75).  Other sets of operands are WIDE: a pre-norm step (residual and next
+// norm alone) 18.1 us forward, 40 backward, a token gate 21.4 and 46.
 enum { ANY, PAIRS, WIDE, FULL };
 
 // Thread `rank` of a group of `size` owns N elements of a row: packs of V, at

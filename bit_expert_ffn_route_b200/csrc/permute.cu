@@ -399,8 +399,8 @@ __global__ void __launch_bounds__(512) permute_rows_shifted_kernel(const T* __re
 // them from all of the token's up to R rows before they add the first; short rows
 // put several tokens in a block.  4,096 tokens x 10 x 3,072 bf16: 45 us, 277 MB at
 // 6.1 TB/s.  EACH: `each` as a constant where U > 1, so that a thread's packs
-// differ by constant offsets (20,011 x 3 x 1,001 fp32: 53 us, 6.0 TB/s; with `each`
-// in a register 72 us).
+// differ by constant offsets (20,011 x 3 x 1,001 fp32: 54 to 55 us, 5.9 TB/s; with
+// `each` in a register 72 us).
 template <typename T, typename TO, int V, int U, int R, int EACH>
 __global__ void __launch_bounds__(kSumThreads) unpermute_kernel(const T* __restrict__ rows, int n_rows,
                                                                 const int32_t* __restrict__ pair_row,
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kDotThreads) unpermute_backward_kernel(const T
 // The same for rows that start anywhere, a block per token: dout[t] in shared
 // memory, rows and drows (which start alike: their buffers are apart by a multiple
 // of 16 bytes) in whole 16-byte blocks, four rows in flight (4,096 x 10 rows of
-// 3,071 bf16: 103 us against 168 us with single elements).
+// 3,071 bf16: 105 us against 168 us with single elements).
 template <typename T, typename TO>
 __global__ void __launch_bounds__(512) unpermute_backward_shifted_kernel(const TO* __restrict__ dout,
                                                                          const T* __restrict__ rows, int n_rows,

@@ -415,10 +415,14 @@ moe_status route_grad_shapes(int T, int D, int E, int k) {
 }
 
 // Few experts, or few more of which a token takes five and more: dense products.
-// Whole calls, dense against pair by pair: 8,266 x 16 of 19 x 256 13 us and 29 us,
-// 20,000 x 2 of 8 x 1,024 26 and 46, 32 x 8 of 16 x 2,048 5.5 and 9.9, 4 tokens 5.9
-// and 5.8; of 32 experts, 1,024 x 4,096, 6 per token 14.9 and 16.0, 4 per token 14.7
-// and 13.0; of 64 (an experts' tile twice as wide) 4,096 x 8 x 2,048 38 and 34.
+// Whole calls, dense against pair by pair: 8,266 x 16 of 19 x 256 13.5 us and 21.5 us,
+// 20,000 x 2 of 8 x 1,024 26 and 43, 32 x 8 of 16 x 2,048 5.3 and 12.3; of 32 experts,
+// 1,024 x 4,096, 6 per token 15.0 and 16.5, 4 per token 14.7 and 13.5, 3 per token 14.8
+// and 12.6; of 64 (an experts' tile twice as wide, by mma.sync as here) 4,096 x 8 x
+// 2,048 38 and 34.  The crossing also moves with T and D, which the rule does not look
+// at: 4,096 x 4 of 32 x 4,096 would be 35 dense and is 42 by pairs, 16,000 x 2 of 32 x
+// 2,048 53 and 60, 4,096 x 4 of 20 x 1,024 14.4 and 16.2; 300 x 1 of 16 x 8,192 is 9.3
+// dense and would be 9.0 by pairs.
 bool route_dense(int T, int E, int k) { return T >= kDenseMinT && (E <= 16 || (E <= kDenseMaxE && k >= 5)); }
 
 // What T tokens need and fewer: the chunks are no more than the blocks of 16 rows, and than kDwSums / D or what chunks

@@ -51,7 +51,7 @@ MOE_DEVINL void store_pack(T* p, const Pack<T, V>& a) {
 // Between loads under a condition and their use under the same one: without it the
 // compiler moves the conversion to fp32 into the load's branch, and each load is
 // waited for before the next is issued (unpermute of 4,096 x 10 rows of 3,071
-// bf16: 184 us against 63 us).
+// bf16: 179 us against 68 us; its gradient 130 us against 107 us).
 template <typename P>
 MOE_DEVINL void hold(P& a) {
     uint32_t* w = reinterpret_cast<uint32_t*>(&a);
