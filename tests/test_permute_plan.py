@@ -1,5 +1,8 @@
 """The plan of large batches in a cluster of 16 blocks and in one of 8, which
 moe_permute takes on a device without room for 16."""
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -44,3 +47,29 @@ def test_both_clusters_sort_alike(T, k, E, kind):
         assert np.array_equal(rp.cpu().numpy()[:len(order)], order) and (rp[len(order):] == -7).all(), blocks
         outs.append((o, pr, rp))
     assert all(torch.equal(a, b) for out in outs[1:] for a, b in zip(outs[0], out))
+
+
+FIRST_CALL = """
+import torch
+from bit_expert_ffn_route_b200 import moe
+T, k, E, D = 1200, 4, 64, 256
+i32 = dict(dtype=torch.int32, device="cuda")
+ids, x = torch.arange(T * k, **i32).view(T, k) % E, torch.randn(T, D, device="cuda")
+o, pr, rp, rows = torch.empty(E + 1, **i32), torch.empty(T, k, **i32), torch.empty(T * k, **i32), torch.empty(T * k, D, device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    moe.moe_permute(ids, E, o, pr, rp, x=x, rows=rows)
+graph.replay()
+torch.cuda.synchronize()
+order = ids.view(-1).sort(stable=True).indices
+assert torch.equal(rp.long(), order) and torch.equal(rows, x[order // k])
+print("ok")
+"""
+
+
+@pytest.mark.gpu
+def test_the_first_call_of_a_process_is_captured():
+    """The question whether a cluster of 16 fits is asked inside the capture."""
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], capture_output=True, text=True, cwd=build.ROOT, timeout=120)
+    assert r.returncode == 0 and r.stdout == "ok\n", (r.stdout, r.stderr)
